@@ -25,7 +25,12 @@ Entry points (same names as the C ABI, without the ``uocr_`` prefix):
   prefix plus the 128-token window (the baselines the sparse step is measured against);
 * :func:`sparse_decode_static` -- the same decode call for callers that cannot
   allocate device memory (scratch held inside the library);
-* :func:`workspace_bytes`.
+* :func:`rope_append_kv8`, :func:`sparse_attn_kv8`, :func:`sparse_decode_kv8`, :func:`dense_decode_kv8`,
+  :func:`sparse_attn_seq_kv8`, :func:`sparse_prefill_kv8` -- the same steps over a key / value cache
+  held in e4m3 with a scale for each (page, head), optionally adding each block's attention weight to
+  its running total;
+* :func:`evict_blocks` -- removes the blocks with the lowest totals from tables, totals and lengths;
+* :func:`workspace_bytes` and its likes.
 """
 from __future__ import annotations
 
@@ -103,6 +108,20 @@ def _load() -> ctypes.CDLL:
     lib.uocr_sparse_attn_seq.restype = I
     lib.uocr_sparse_decode_static.argtypes = [P, P, P, P, P, P, P, I, I, I, I, P, P, P, P]
     lib.uocr_sparse_decode_static.restype = I
+    lib.uocr_rope_append_kv8.argtypes = [P] * 10 + [I] * 5 + [P] * 9
+    lib.uocr_sparse_attn_kv8.argtypes = [P] * 10 + [I] * 5 + [F, P, P, P, P]
+    lib.uocr_sparse_decode_kv8.argtypes = [P] * 9 + [I] * 4 + [P, P, P, P, Z, P, P]
+    lib.uocr_dense_decode_kv8.argtypes = [P] * 7 + [I] * 5 + [P, P, P, Z, P, P]
+    lib.uocr_sparse_attn_seq_kv8.argtypes = [P] * 7 + [I, P, P] + [I] * 5 + [F, P, P, P, Z, P, P]
+    lib.uocr_sparse_prefill_kv8.argtypes = [P] * 9 + [I, P] + [I] * 5 + [P, P, P, P, Z, P, P]
+    lib.uocr_evict_blocks.argtypes = [P] * 3 + [I] * 5 + [P] * 6 + [Z, P, P]
+    for name in ("rope_append_kv8", "sparse_attn_kv8", "sparse_decode_kv8", "dense_decode_kv8", "sparse_attn_seq_kv8",
+                 "sparse_prefill_kv8", "evict_blocks"):
+        getattr(lib, "uocr_" + name).restype = I
+    for name in ("dense_kv8", "sparse_attn_seq_kv8", "prefill_kv8", "evict"):
+        fn = getattr(lib, f"uocr_{name}_workspace_bytes")
+        fn.argtypes = [I, I, I]
+        fn.restype = Z
     return lib
 
 
@@ -570,3 +589,282 @@ def sparse_decode_static(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, s
         _ptr(seq_lens), B, H, block_table.shape[1], k_cache.shape[0], _ptr(out), _ptr(sel),
         _ptr(dev_err), _stream(stream)))
     return out, sel
+
+
+# --------------------------------------------------------------------------- the cache held in 8 bits
+def dense_kv8_workspace_bytes(n_q: int, heads: int, max_blocks: int) -> int:
+    return int(_lib().uocr_dense_kv8_workspace_bytes(int(n_q), int(heads), int(max_blocks)))
+
+
+def sparse_attn_seq_kv8_workspace_bytes(n_q: int, heads: int, max_blocks: int) -> int:
+    return int(_lib().uocr_sparse_attn_seq_kv8_workspace_bytes(int(n_q), int(heads), int(max_blocks)))
+
+
+def prefill_kv8_workspace_bytes(n_q: int, heads: int, max_blocks: int) -> int:
+    return int(_lib().uocr_prefill_kv8_workspace_bytes(int(n_q), int(heads), int(max_blocks)))
+
+
+def evict_workspace_bytes(n_seq: int, heads: int, max_blocks: int) -> int:
+    return int(_lib().uocr_evict_workspace_bytes(int(n_seq), int(heads), int(max_blocks)))
+
+
+def _one_device(*tensors):
+    """The device of all the given tensors (None among them is skipped)."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return dev
+
+
+def _launch(fn: str, dev, stream, *args):
+    """Call uocr_<fn>(*args, stream) with `dev` current, on its current stream unless one is given."""
+    with torch.cuda.device(dev):
+        s = torch.cuda.current_stream(dev) if stream is None else stream
+        _check("uocr_" + fn, getattr(_lib(), "uocr_" + fn)(*args, ctypes.c_void_p(s.cuda_stream)))
+
+
+def _workspace(workspace, nbytes: int, dev) -> torch.Tensor:
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
+    return _dev(workspace, "workspace", torch.uint8, 1)
+
+
+def _check_kv8(k_cache, v_cache, k_scale, v_scale, H):
+    """e4m3 caches [P, H, 32, 128] and their fp32 scales [P, H]."""
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _dev(t, n, torch.float8_e4m3fn, 4)
+    _check_caches(k_cache, v_cache, H)
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _dev(t, n, torch.float32, 2)
+        _shape(t, n, (k_cache.shape[0], H))
+
+
+def _check_seqs(block_table, seq_lens, B=None):
+    _dev(block_table, "block_table", torch.int32, 2)
+    _dev(seq_lens, "seq_lens", torch.int32, 1)
+    _shape(block_table, "block_table", (B, None))
+    _shape(seq_lens, "seq_lens", (block_table.shape[0],))
+
+
+def _check_mass(mass, B, H, mb):
+    if mass is not None:
+        _dev(mass, "mass", torch.float32, 3)
+        _shape(mass, "mass", (B, H, mb))
+
+
+def _out(out, q):
+    if out is None:
+        return torch.empty_like(q)
+    _dev(out, "out", torch.bfloat16, 3)
+    return _shape(out, "out", tuple(q.shape))
+
+
+def _dev_err(dev_err):
+    if dev_err is not None:
+        _dev(dev_err, "dev_err", torch.int32)
+        if dev_err.numel() < 1:
+            raise ValueError("dev_err must hold one int32")
+    return dev_err
+
+
+def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_table, seq_lens, k_cache, v_cache,
+                    k_scale, v_scale, idx_k_cache, new_start=None, *, q_out=None, idx_q_out=None, dev_err=None,
+                    stream=None):
+    """Rotate q / idx_q (page2d; in place unless q_out / idx_q_out are given) and append the new tokens: rotated k
+    and raw v quantised to e4m3 under one power-of-two scale per (page, head), rotated idx_k as bf16.  Sequence b's
+    new tokens are rows new_start[b] .. new_start[b + 1] - 1 (None: token i belongs to sequence i) and take the
+    sequence's last positions.  Returns (q_out, idx_q_out)."""
+    for t, n, dt, nd in ((q, "q", torch.bfloat16, 3), (idx_q, "idx_q", torch.bfloat16, 2),
+                         (k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
+                         (idx_k_new, "idx_k_new", torch.bfloat16, 2), (tok_pos, "tok_pos", torch.int32, 1),
+                         (page_pos, "page_pos", torch.int32, 1), (idx_k_cache, "idx_k_cache", torch.bfloat16, 3)):
+        _dev(t, n, dt, nd)
+    n, H = q.shape[0], q.shape[1]
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens)
+    B, mb = block_table.shape
+    _shape(q, "q", (n, H, HEAD_DIM))
+    _shape(idx_q, "idx_q", (n, IDX_DIM))
+    _shape(k_new, "k_new", (n, H, HEAD_DIM))
+    _shape(v_new, "v_new", (n, H, HEAD_DIM))
+    _shape(idx_k_new, "idx_k_new", (n, IDX_DIM))
+    _shape(tok_pos, "tok_pos", (n,))
+    _shape(page_pos, "page_pos", (n,))
+    _shape(idx_k_cache, "idx_k_cache", (k_cache.shape[0], BLOCK, IDX_DIM))
+    _opt_i32(new_start, "new_start", B + 1)
+    q_out = q if q_out is None else _out(q_out, q)
+    if idx_q_out is None:
+        idx_q_out = idx_q
+    _dev(idx_q_out, "idx_q_out", torch.bfloat16, 2)
+    _shape(idx_q_out, "idx_q_out", (n, IDX_DIM))
+    dev = _one_device(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_table, seq_lens, k_cache, v_cache,
+                      k_scale, v_scale, idx_k_cache, new_start, q_out, idx_q_out, _dev_err(dev_err))
+    _launch("rope_append_kv8", dev, stream, _ptr(q), _ptr(idx_q), _ptr(k_new), _ptr(v_new), _ptr(idx_k_new),
+            _ptr(tok_pos), _ptr(page_pos), _ptr(new_start), _ptr(block_table), _ptr(seq_lens), n, B, H, mb,
+            k_cache.shape[0], _ptr(q_out), _ptr(idx_q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+            _ptr(v_scale), _ptr(idx_k_cache), _ptr(dev_err))
+    return q_out, idx_q_out
+
+
+def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sel, q_seq=None, q_pos=None, *,
+                    scale: float | None = None, out=None, mass=None, dev_err=None, stream=None) -> torch.Tensor:
+    """sparse_attn over the 8-bit cache: bf16 [n_q, H, 128].  mass [B, H, max_blocks] fp32 (one query per
+    sequence, q_seq None): each selected block's attention weight is added to its total."""
+    _dev(q, "q", torch.bfloat16, 3)
+    n_q, H = q.shape[0], q.shape[1]
+    _shape(q, "q", (n_q, H, HEAD_DIM))
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens)
+    B, mb = block_table.shape
+    _dev(sel, "sel", torch.int32, 2)
+    _shape(sel, "sel", (n_q, N_SEL))
+    _opt_i32(q_seq, "q_seq", n_q)
+    _opt_i32(q_pos, "q_pos", n_q)
+    _check_mass(mass, B, H, mb)
+    if mass is not None and q_seq is not None:
+        raise ValueError("mass needs one query per sequence: q_seq must be None")
+    out = _out(out, q)
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sel, q_seq, q_pos, out, mass,
+                      _dev_err(dev_err))
+    sc = float(scale) if scale is not None else HEAD_DIM ** -0.5
+    _launch("sparse_attn_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), _ptr(seq_lens), _ptr(q_seq), _ptr(q_pos), _ptr(sel), n_q, B, H, mb, k_cache.shape[0],
+            sc, _ptr(out), _ptr(mass), _ptr(dev_err))
+    return out
+
+
+def sparse_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, *, out=None,
+                      sel=None, mass=None, workspace=None, dev_err=None, stream=None):
+    """sparse_decode over the 8-bit cache.  Returns (out [B,H,128] bf16, sel [B,16] int32)."""
+    _dev(q, "q", torch.bfloat16, 3)
+    _dev(idx_q, "idx_q", torch.bfloat16, 2)
+    _dev(idx_k_cache, "idx_k_cache", torch.bfloat16, 3)
+    B, H = q.shape[0], q.shape[1]
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens, B)
+    mb = block_table.shape[1]
+    out = _out(out, q)
+    if sel is None:
+        sel = torch.empty((B, N_SEL), dtype=torch.int32, device=q.device)
+    _dev(sel, "sel", torch.int32, 2)
+    _check_decode_args(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_lens, out, sel)
+    _check_mass(mass, B, H, mb)
+    workspace = _workspace(workspace, workspace_bytes(B, H, mb), q.device)
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, out, sel,
+                      mass, workspace, _dev_err(dev_err))
+    _launch("sparse_decode_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(idx_q), _ptr(idx_k_cache), _ptr(block_table), _ptr(seq_lens), B, H, mb, k_cache.shape[0], _ptr(out),
+            _ptr(sel), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+    return out, sel
+
+
+def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, *, ref_blocks: int | None = None,
+                     out=None, mass=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
+    """dense_decode over the 8-bit cache: blocks [0, ref_blocks) plus the 4-block local window, or all of them
+    when ref_blocks is None.  Returns out [B,H,128] bf16; mass [B, H, max_blocks] receives every attended block's
+    weight."""
+    _dev(q, "q", torch.bfloat16, 3)
+    B, H = q.shape[0], q.shape[1]
+    _shape(q, "q", (B, H, HEAD_DIM))
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens, B)
+    mb = block_table.shape[1]
+    rb = mb if ref_blocks is None else int(ref_blocks)
+    _check_mass(mass, B, H, mb)
+    out = _out(out, q)
+    workspace = _workspace(workspace, dense_kv8_workspace_bytes(B, H, mb), q.device)
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, mass, workspace,
+                      _dev_err(dev_err))
+    _launch("dense_decode_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), _ptr(seq_lens), rb, B, H, mb, k_cache.shape[0], _ptr(out), _ptr(mass), _ptr(workspace),
+            workspace.numel(), _ptr(dev_err))
+    return out
+
+
+def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, seq: int, q_pos, sel, *,
+                        scale: float | None = None, out=None, mass=None, workspace=None, dev_err=None,
+                        stream=None) -> torch.Tensor:
+    """sparse_attn_seq over the 8-bit cache: many queries of sequence `seq` over the given selection.  Returns out
+    [n_q,H,128] bf16; row `seq` of mass [B, H, max_blocks] receives the queries' weights."""
+    _dev(q, "q", torch.bfloat16, 3)
+    n_q, H = q.shape[0], q.shape[1]
+    _shape(q, "q", (n_q, H, HEAD_DIM))
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens)
+    B, mb = block_table.shape
+    _dev(q_pos, "q_pos", torch.int32, 1)
+    _shape(q_pos, "q_pos", (n_q,))
+    _dev(sel, "sel", torch.int32, 2)
+    _shape(sel, "sel", (n_q, N_SEL))
+    _check_mass(mass, B, H, mb)
+    out = _out(out, q)
+    workspace = _workspace(workspace, sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), q.device)
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_pos, sel, out, mass, workspace,
+                      _dev_err(dev_err))
+    sc = float(scale) if scale is not None else HEAD_DIM ** -0.5
+    _launch("sparse_attn_seq_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(block_table), _ptr(seq_lens), int(seq), _ptr(q_pos), _ptr(sel), n_q, B, H, mb, k_cache.shape[0], sc,
+            _ptr(out), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+    return out
+
+
+def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, seq: int,
+                       q_pos, *, out=None, sel=None, mass=None, workspace=None, dev_err=None, stream=None):
+    """sparse_prefill over the 8-bit cache.  Returns (out [n_q,H,128] bf16, sel [n_q,16] int32)."""
+    _dev(q, "q", torch.bfloat16, 3)
+    _dev(idx_q, "idx_q", torch.bfloat16, 2)
+    _dev(idx_k_cache, "idx_k_cache", torch.bfloat16, 3)
+    _dev(q_pos, "q_pos", torch.int32, 1)
+    n_q, H = q.shape[0], q.shape[1]
+    _shape(q, "q", (n_q, H, HEAD_DIM))
+    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
+    _check_seqs(block_table, seq_lens)
+    B, mb = block_table.shape
+    _shape(idx_q, "idx_q", (n_q, IDX_DIM))
+    _shape(idx_k_cache, "idx_k_cache", (k_cache.shape[0], BLOCK, IDX_DIM))
+    _shape(q_pos, "q_pos", (n_q,))
+    if sel is None:
+        sel = torch.empty((n_q, N_SEL), dtype=torch.int32, device=q.device)
+    _dev(sel, "sel", torch.int32, 2)
+    _shape(sel, "sel", (n_q, N_SEL))
+    _check_mass(mass, B, H, mb)
+    out = _out(out, q)
+    workspace = _workspace(workspace, prefill_kv8_workspace_bytes(n_q, H, mb), q.device)
+    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, q_pos, out,
+                      sel, mass, workspace, _dev_err(dev_err))
+    _launch("sparse_prefill_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+            _ptr(idx_q), _ptr(idx_k_cache), _ptr(block_table), _ptr(seq_lens), int(seq), _ptr(q_pos), n_q, B, H, mb,
+            k_cache.shape[0], _ptr(out), _ptr(sel), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+    return out, sel
+
+
+def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int = 0, new_mass=None, new_table=None,
+                 new_lens=None, freed=None, n_freed=None, workspace=None, dev_err=None, stream=None):
+    """Cut every sequence of more than keep_blocks blocks to keep_blocks: its first n_sink blocks, its 4 local ones
+    and those of the others with the highest totals over the heads (lower id on ties) stay.  Returns (new_mass
+    [B,H,max_blocks] fp32, new_table [B,max_blocks] int32, new_lens [B] int32, freed [B,max_blocks] int32 pages,
+    n_freed [B] int32); the first three may be the inputs themselves."""
+    _dev(mass, "mass", torch.float32, 3)
+    _check_seqs(block_table, seq_lens)
+    B, mb = block_table.shape
+    H = mass.shape[1]
+    _check_mass(mass, B, H, mb)
+    new_mass = torch.empty_like(mass) if new_mass is None else new_mass
+    new_table = torch.empty_like(block_table) if new_table is None else new_table
+    new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
+    freed = torch.empty_like(block_table) if freed is None else freed
+    n_freed = torch.empty_like(seq_lens) if n_freed is None else n_freed
+    _dev(new_mass, "new_mass", torch.float32, 3)
+    _shape(new_mass, "new_mass", (B, H, mb))
+    for t, n, shape in ((new_table, "new_table", (B, mb)), (new_lens, "new_lens", (B,)), (freed, "freed", (B, mb)),
+                        (n_freed, "n_freed", (B,))):
+        _dev(t, n, torch.int32, len(shape))
+        _shape(t, n, shape)
+    workspace = _workspace(workspace, evict_workspace_bytes(B, H, mb), mass.device)
+    dev = _one_device(mass, block_table, seq_lens, new_mass, new_table, new_lens, freed, n_freed, workspace,
+                      _dev_err(dev_err))
+    _launch("evict_blocks", dev, stream, _ptr(mass), _ptr(block_table), _ptr(seq_lens), B, H, mb, int(keep_blocks),
+            int(n_sink), _ptr(new_mass), _ptr(new_table), _ptr(new_lens), _ptr(freed), _ptr(n_freed), _ptr(workspace),
+            workspace.numel(), _ptr(dev_err))
+    return new_mass, new_table, new_lens, freed, n_freed

@@ -426,4 +426,259 @@ uocr_status_t uocr_block_topk_masked(const float *scores, const int32_t *seq_len
                                                -1, cand_mask, mask_words));
 }
 
+// ------------------------------------------------------------------ the cache held in e4m3, eviction
+}  // extern "C"
+
+namespace {
+inline bool f32_ok(const void *p) { return p && aligned(p, 4); }
+
+// The checks that every entry point over the 8-bit cache shares.
+inline uocr_status_t check_kv8(const void *k_cache, const void *v_cache, const float *k_scale, const float *v_scale,
+                               int H) {
+    if (!bf16_ok(k_cache) || !bf16_ok(v_cache) || !f32_ok(k_scale) || !f32_ok(v_scale)) return UOCR_ERR_INVALID_ARG;
+    if (H < 1 || H > UOCR_MAX_HEADS) return UOCR_ERR_UNSUPPORTED;
+    return UOCR_OK;
+}
+inline bool mass_ok(const float *mass) { return !mass || aligned(mass, 4); }
+
+// Two arrays of the given bytes that are neither the same nor apart.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb, bool same_ok) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    if (same_ok && x == y) return false;
+    return x < y + nb && y < x + na;
+}
+}  // namespace
+
+extern "C" {
+
+uocr_status_t uocr_rope_append_kv8(const void *q, const void *idx_q, const void *k_new, const void *v_new,
+                                   const void *idx_k_new, const int32_t *tok_pos, const int32_t *page_pos,
+                                   const int32_t *new_start, const int32_t *block_table, const int32_t *seq_lens,
+                                   int n, int B, int H, int max_blocks, int num_pages, void *q_out, void *idx_q_out,
+                                   void *k_cache, void *v_cache, float *k_scale, float *v_scale, void *idx_k_cache,
+                                   int32_t *dev_err, uocr_stream_t stream) {
+    uocr_status_t st = check_common(n, B, max_blocks, num_pages, block_table, seq_lens, nullptr, nullptr, dev_err);
+    if (st != UOCR_OK) return st;
+    if (!new_start && n != B) return UOCR_ERR_INVALID_ARG;   // one new token per sequence
+    if (n == 0) return UOCR_OK;
+    if (!bf16_ok(q) || !bf16_ok(idx_q) || !bf16_ok(k_new) || !bf16_ok(v_new) || !bf16_ok(idx_k_new) ||
+        !bf16_ok(q_out) || !bf16_ok(idx_q_out) || !bf16_ok(idx_k_cache))
+        return UOCR_ERR_INVALID_ARG;
+    if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
+    if (!tok_pos || !page_pos || !aligned(tok_pos, 4) || !aligned(page_pos, 4)) return UOCR_ERR_INVALID_ARG;
+    if (new_start && !aligned(new_start, 4)) return UOCR_ERR_INVALID_ARG;
+    const size_t q_bytes = (size_t)n * H * UOCR_HEAD_DIM * 2, i_bytes = (size_t)n * UOCR_IDX_DIM * 2;
+    if (overlap(q, q_bytes, q_out, q_bytes, true) || overlap(idx_q, i_bytes, idx_q_out, i_bytes, true))
+        return UOCR_ERR_INVALID_ARG;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    return cuda_status(uocr::launch_rope_append_kv8(c, q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, new_start,
+                                                    block_table, seq_lens, n, B, H, max_blocks, num_pages, q_out,
+                                                    idx_q_out, k_cache, v_cache, k_scale, v_scale, idx_k_cache,
+                                                    dev_err));
+}
+
+uocr_status_t uocr_sparse_attn_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                   const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *q_seq, const int32_t *q_pos, const int32_t *sel, int n_q, int B,
+                                   int H, int max_blocks, int num_pages, float scale, void *out, float *mass,
+                                   int32_t *dev_err, uocr_stream_t stream) {
+    uocr_status_t st = check_common(n_q, B, max_blocks, num_pages, block_table, seq_lens, q_seq, q_pos, dev_err);
+    if (st != UOCR_OK) return st;
+    if (!isfinite(scale)) return UOCR_ERR_INVALID_ARG;
+    if (mass && q_seq) return UOCR_ERR_INVALID_ARG;   // a total has one writer: one query per sequence
+    if (n_q == 0) return UOCR_OK;
+    if (!bf16_ok(q) || !bf16_ok(out) || !sel || !aligned(sel, 4) || !mass_ok(mass)) return UOCR_ERR_INVALID_ARG;
+    if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
+    return cuda_status(uocr::launch_sparse_attn_kv8(c, q, kv, block_table, seq_lens, q_seq, q_pos, sel, n_q, B, H,
+                                                    max_blocks, num_pages, scale, out, mass, false, dev_err));
+}
+
+uocr_status_t uocr_sparse_decode_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                     const float *v_scale, const void *idx_q, const void *idx_k_cache,
+                                     const int32_t *block_table, const int32_t *seq_lens, int B, int H,
+                                     int max_blocks, int num_pages, void *out, int32_t *sel_out, float *mass,
+                                     void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                     uocr_stream_t stream) {
+    uocr_status_t st = uocr::check_sparse_decode_args(q, k_cache, v_cache, idx_q, idx_k_cache, block_table,
+                                                      seq_lens, B, H, max_blocks, num_pages, out, sel_out, dev_err);
+    if (st != UOCR_OK) return st;
+    if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
+    if (!mass_ok(mass)) return UOCR_ERR_INVALID_ARG;
+    const WsLayout w = ws_layout(B, H, max_blocks);
+    if (!workspace || !aligned(workspace, kWsAlign) || workspace_bytes < w.total) return UOCR_ERR_WORKSPACE;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    float *scores = (float *)((char *)workspace + w.scores_off);
+    cudaError_t e = uocr::launch_index_scan(c, idx_q, idx_k_cache, block_table, seq_lens, nullptr, nullptr, B, B,
+                                            max_blocks, num_pages, scores, dev_err);
+    if (e != cudaSuccess) return cuda_status(e);
+    c.pdl = true;
+    e = uocr::launch_block_topk(c, scores, seq_lens, nullptr, nullptr, B, B, max_blocks, sel_out, dev_err);
+    if (e != cudaSuccess) return cuda_status(e);
+    const float scale = 1.0f / sqrtf((float)UOCR_HEAD_DIM);
+    const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
+    return cuda_status(uocr::launch_sparse_attn_kv8(c, q, kv, block_table, seq_lens, nullptr, nullptr, sel_out, B, B,
+                                                    H, max_blocks, num_pages, scale, out, mass, true, dev_err));
+}
+
+size_t uocr_dense_kv8_workspace_bytes(int B, int H, int max_blocks) {
+    if (B <= 0 || H <= 0 || max_blocks <= 0) return 0;
+    return uocr::dense_kv8_workspace(B, H, max_blocks);
+}
+
+uocr_status_t uocr_dense_decode_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                    const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                    int ref_blocks, int B, int H, int max_blocks, int num_pages, void *out,
+                                    float *mass, void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                    uocr_stream_t stream) {
+    uocr_status_t st = check_common(B, B, max_blocks, num_pages, block_table, seq_lens, nullptr, nullptr, dev_err);
+    if (st != UOCR_OK) return st;
+    if (!bf16_ok(q) || !bf16_ok(out) || ref_blocks < 0 || !mass_ok(mass)) return UOCR_ERR_INVALID_ARG;
+    if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
+    if (!workspace || !aligned(workspace, kWsAlign) ||
+        workspace_bytes < uocr_dense_kv8_workspace_bytes(B, H, max_blocks))
+        return UOCR_ERR_WORKSPACE;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    const float scale = 1.0f / sqrtf((float)UOCR_HEAD_DIM);
+    const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
+    return cuda_status(uocr::launch_dense_kv8(c, q, kv, block_table, seq_lens, B, H, max_blocks, num_pages, ref_blocks,
+                                              scale, out, mass, workspace, dev_err));
+}
+
+size_t uocr_sparse_attn_seq_kv8_workspace_bytes(int n_q, int H, int max_blocks) {
+    if (n_q <= 0 || H <= 0 || max_blocks <= 0) return 0;
+    return uocr::prefill_kv8_workspace(n_q, H, max_blocks);
+}
+
+size_t uocr_prefill_kv8_workspace_bytes(int n_q, int H, int max_blocks) {
+    if (n_q <= 0 || H <= 0 || max_blocks <= 0) return 0;
+    return ws_layout(n_q, H, max_blocks).total + uocr::prefill_kv8_workspace(n_q, H, max_blocks);
+}
+
+}  // extern "C"
+
+namespace {
+// The checks that the two many-query forms over the 8-bit cache share.
+inline uocr_status_t check_seq_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                   const float *v_scale, const int32_t *block_table, const int32_t *seq_lens, int seq,
+                                   const int32_t *q_pos, const int32_t *sel, int n_q, int B, int H, int max_blocks,
+                                   int num_pages, const void *out, const float *mass, const int32_t *dev_err) {
+    uocr_status_t st = check_common(n_q, B, max_blocks, num_pages, block_table, seq_lens, nullptr, q_pos, dev_err);
+    if (st != UOCR_OK) return st;
+    if (seq < 0 || seq >= B) return UOCR_ERR_INVALID_ARG;
+    if (n_q == 0) return UOCR_OK;
+    if (!bf16_ok(q) || !bf16_ok(out) || !q_pos || !sel || !aligned(sel, 4) || !mass_ok(mass))
+        return UOCR_ERR_INVALID_ARG;
+    if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
+    if ((long long)n_q * UOCR_N_SEL > 0x7fffffffLL || (long long)n_q * H > 0x7fffffffLL / 2) return UOCR_ERR_UNSUPPORTED;
+    // units of work and block totals are counted in int32
+    if ((long long)uocr::prefill_item_bound(n_q, max_blocks) * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;
+    if ((long long)max_blocks * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;
+    return UOCR_OK;
+}
+}  // namespace
+
+extern "C" {
+
+uocr_status_t uocr_sparse_attn_seq_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                       int seq, const int32_t *q_pos, const int32_t *sel, int n_q, int B, int H,
+                                       int max_blocks, int num_pages, float scale, void *out, float *mass,
+                                       void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                       uocr_stream_t stream) {
+    uocr_status_t st = check_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, seq, q_pos, sel, n_q,
+                                     B, H, max_blocks, num_pages, out, mass, dev_err);
+    if (st != UOCR_OK) return st;
+    if (!isfinite(scale)) return UOCR_ERR_INVALID_ARG;
+    if (n_q == 0) return UOCR_OK;
+    if (!workspace || !aligned(workspace, kWsAlign) ||
+        workspace_bytes < uocr_sparse_attn_seq_kv8_workspace_bytes(n_q, H, max_blocks))
+        return UOCR_ERR_WORKSPACE;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    cudaError_t e = uocr::zero_prefill_kv8(c, workspace, n_q, H, max_blocks, nullptr);
+    if (e != cudaSuccess) return cuda_status(e);
+    const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
+    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, block_table + (size_t)seq * max_blocks, seq_lens + seq,
+                                                q_pos, sel, n_q, H, max_blocks, num_pages, scale, out,
+                                                mass ? mass + (size_t)seq * H * max_blocks : nullptr, workspace,
+                                                dev_err));
+}
+
+uocr_status_t uocr_sparse_prefill_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                      const float *v_scale, const void *idx_q, const void *idx_k_cache,
+                                      const int32_t *block_table, const int32_t *seq_lens, int seq,
+                                      const int32_t *q_pos, int n_q, int B, int H, int max_blocks, int num_pages,
+                                      void *out, int32_t *sel_out, float *mass, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_err, uocr_stream_t stream) {
+    uocr_status_t st = check_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, seq, q_pos, sel_out,
+                                     n_q, B, H, max_blocks, num_pages, out, mass, dev_err);
+    if (st != UOCR_OK || n_q == 0) return st;
+    if (!bf16_ok(idx_q) || !bf16_ok(idx_k_cache)) return UOCR_ERR_INVALID_ARG;
+    const WsLayout w = ws_layout(n_q, H, max_blocks);
+    if (!workspace || !aligned(workspace, kWsAlign) ||
+        workspace_bytes < uocr_prefill_kv8_workspace_bytes(n_q, H, max_blocks))
+        return UOCR_ERR_WORKSPACE;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    float *scores = (float *)((char *)workspace + w.scores_off);
+    char *attn_ws = (char *)workspace + w.total;
+    int32_t *sched = nullptr;
+    cudaError_t e = uocr::zero_prefill_kv8(c, attn_ws, n_q, H, max_blocks, &sched);
+    if (e != cudaSuccess) return cuda_status(e);
+    const int32_t *bt_row = block_table + (size_t)seq * max_blocks;
+    e = uocr::launch_prefill_index_gemm(c, idx_q, idx_k_cache, bt_row, seq_lens + seq, q_pos, n_q, max_blocks,
+                                        num_pages, scores, sched, dev_err);
+    if (e != cudaSuccess) return cuda_status(e);
+    c.pdl = true;
+    e = uocr::launch_block_topk(c, scores, seq_lens, nullptr, q_pos, n_q, B, max_blocks, sel_out, dev_err, seq);
+    if (e != cudaSuccess) return cuda_status(e);
+    const float scale = 1.0f / sqrtf((float)UOCR_HEAD_DIM);
+    const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
+    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, bt_row, seq_lens + seq, q_pos, sel_out, n_q, H, max_blocks,
+                                                num_pages, scale, out,
+                                                mass ? mass + (size_t)seq * H * max_blocks : nullptr, attn_ws,
+                                                dev_err));
+}
+
+size_t uocr_evict_workspace_bytes(int B, int H, int max_blocks) {
+    if (B <= 0 || H <= 0 || max_blocks <= 0) return 0;
+    return uocr::evict_workspace(B, max_blocks);
+}
+
+uocr_status_t uocr_evict_blocks(const float *mass, const int32_t *block_table, const int32_t *seq_lens, int B, int H,
+                                int max_blocks, int keep_blocks, int n_sink, float *new_mass, int32_t *new_table,
+                                int32_t *new_lens, int32_t *freed, int32_t *n_freed, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_err, uocr_stream_t stream) {
+    uocr_status_t st = check_common(B, B, max_blocks, 1, block_table, seq_lens, nullptr, nullptr, dev_err);
+    if (st != UOCR_OK) return st;
+    if (!f32_ok(mass) || !f32_ok(new_mass) || !f32_ok(new_table) || !f32_ok(new_lens) || !f32_ok(freed) ||
+        !f32_ok(n_freed))
+        return UOCR_ERR_INVALID_ARG;
+    if (H < 1 || H > UOCR_MAX_HEADS) return UOCR_ERR_UNSUPPORTED;
+    if (n_sink < 0 || n_sink > max_blocks || keep_blocks < UOCR_N_LOCAL + n_sink) return UOCR_ERR_INVALID_ARG;
+    const size_t table = (size_t)B * max_blocks * 4, totals = table * H, lens = (size_t)B * 4;
+    // an output may be its input; any other overlap would be read after it is written
+    const void *in[3] = {mass, block_table, seq_lens};
+    const void *out[5] = {new_mass, new_table, new_lens, freed, n_freed};
+    const size_t in_bytes[3] = {totals, table, lens}, out_bytes[5] = {totals, table, lens, table, lens};
+    for (int o = 0; o < 5; ++o) {
+        for (int i = 0; i < 3; ++i)
+            if (overlap(out[o], out_bytes[o], in[i], in_bytes[i], o == i)) return UOCR_ERR_INVALID_ARG;
+        for (int p = 0; p < o; ++p)
+            if (overlap(out[o], out_bytes[o], out[p], out_bytes[p], false)) return UOCR_ERR_INVALID_ARG;
+    }
+    if (!workspace || !aligned(workspace, kWsAlign) || workspace_bytes < uocr_evict_workspace_bytes(B, H, max_blocks))
+        return UOCR_ERR_WORKSPACE;
+    uocr::LaunchCtx c;
+    if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
+    return cuda_status(uocr::launch_evict(c, mass, block_table, seq_lens, B, H, max_blocks, keep_blocks, n_sink,
+                                          new_mass, new_table, new_lens, freed, n_freed, workspace, dev_err));
+}
+
 }  // extern "C"

@@ -91,6 +91,13 @@ cudaError_t launch_prefill_local(const LaunchCtx &c, const void *q, const void *
 cudaError_t launch_prefill_merge(const LaunchCtx &c, const int32_t *sel_ws, const void *part_o, const float *part_ml,
                                  const void *loc_o, const float2 *loc_ml, int n_q, int H, void *out);
 
+// The inversion of a (classified) selection into items of at most 16 entries per block, and a bound
+// on their number.
+size_t prefill_item_bound(int n_q, int max_blocks);
+cudaError_t launch_prefill_invert(const LaunchCtx &c, const int32_t *counts, const int32_t *bt_row,
+                                  const int32_t *sel_ws, const int32_t *q_pos, int n_q, int max_blocks, int32_t *fill,
+                                  int4 *items, int32_t *n_items, int2 *list);
+
 // Comparator decode attention over [0, min(ref_blocks, nb)) U the 4-block local window.
 int dense_chunks(int max_blocks);
 size_t dense_attn_workspace(int n_q, int H, int max_blocks);
@@ -115,5 +122,40 @@ cudaError_t launch_summary_scan(const LaunchCtx &c, const void *idx_q, const voi
                                 int max_blocks, int num_pages, float *scores, int32_t *dev_err);
 cudaError_t launch_block_mean(const LaunchCtx &c, const void *idx_k, const int32_t *pages, int n_pages,
                               int num_pages, void *summary, int32_t *dev_err);
+
+// The cache held in e4m3: codes [P][H][32][128], scales [P][H].
+struct Kv8Cache {
+    const void *k, *v;
+    const float *k_scale, *v_scale;
+};
+cudaError_t launch_rope_append_kv8(const LaunchCtx &c, const void *q, const void *idx_q, const void *k_new,
+                                   const void *v_new, const void *idx_k_new, const int32_t *tok_pos,
+                                   const int32_t *page_pos, const int32_t *start, const int32_t *bt,
+                                   const int32_t *seq_lens, int n, int B, int H, int max_blocks, int num_pages,
+                                   void *q_out, void *idx_q_out, void *k_cache, void *v_cache, float *k_scale,
+                                   float *v_scale, void *idx_k_cache, int32_t *dev_err);
+// mass [B][H][max_blocks] or NULL (q_seq NULL then: one query per sequence).
+cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
+                                   const int32_t *seq_lens, const int32_t *q_seq, const int32_t *q_pos,
+                                   const int32_t *sel, int n_q, int B, int H, int max_blocks, int num_pages,
+                                   float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err);
+size_t dense_kv8_workspace(int n_q, int H, int max_blocks);
+cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
+                             const int32_t *seq_lens, int B, int H, int max_blocks, int num_pages, int ref_blocks,
+                             float scale, void *out, float *mass, void *ws, int32_t *dev_err);
+size_t prefill_kv8_workspace(int n_q, int H, int max_blocks);
+// Zeroes what launch_prefill_kv8 needs zero; *sched: the scoring GEMM's zeroed work-unit counter.
+cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, int32_t **sched);
+// mass_row [H][max_blocks] of the sequence, or NULL.
+cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt_row,
+                               const int32_t *seq_len_ptr, const int32_t *q_pos, const int32_t *sel, int n_q, int H,
+                               int max_blocks, int num_pages, float scale, void *out, float *mass_row, void *ws,
+                               int32_t *dev_err);
+
+// Eviction of blocks by accumulated attention weight.
+size_t evict_workspace(int B, int max_blocks);
+cudaError_t launch_evict(const LaunchCtx &c, const float *mass, const int32_t *table, const int32_t *seq_lens, int B,
+                         int H, int max_blocks, int keep_blocks, int n_sink, float *new_mass, int32_t *new_table,
+                         int32_t *new_lens, int32_t *freed, int32_t *n_freed, void *ws, int32_t *dev_err);
 
 }  // namespace uocr

@@ -1,0 +1,198 @@
+// kv8.cuh -- warp-level tile products over a key / value cache held in 8 bits (e4m3).
+//
+// Cache layout: codes [P][H][32][128] of one byte (a (page, head) tile is 4 KiB, contiguous) and
+// one fp32 scale per (page, head) for K and one for V: value = code * scale.  An e4m3 code is an
+// fp16 number exactly (4 significant bits, 2^-9 .. 448), so the tile products run on the fp16
+// tensor cores with fp32 accumulation and the scale is applied to their fp32 results: neither K
+// nor V is rounded again.
+//
+// Fragments.  The contraction index of an MMA may be permuted as long as both operands agree, so
+// lane (g, c) = (lane / 4, lane % 4) takes its operand elements as whole 16-byte pieces of a row,
+// straight from global memory into registers (no staging, no shuffles, full 32-byte sectors):
+//   K, rows g + 8 i (i = 0..3): pieces c and c + 4 of the row (dims 16 c .. + 15 and 64 + 16 c .. + 15);
+//      word w of piece f holds the 4 dims of one 16-dim MMA step (f, w), two per operand register;
+//   V: piece g (dims 16 g .. 16 g + 15) of 4 tokens per 16-token MMA step; a byte permute pairs two
+//      tokens' codes of one dim, which is what one operand register holds.
+// These are the warp-level MMAs (m16n8k16): a decode step has one query row per (sequence, head),
+// and an item of a prefill chunk at most 16, far below the 64-row tile of tcgen05; the products
+// are a small part of the time, the point is to take the conversion, the dot products and their
+// reductions off the FMA pipes.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+
+namespace uocr {
+
+constexpr int kTile8 = kBlock * kD;        // bytes of one (page, head) tile of codes
+constexpr int kTile8U4 = kTile8 / 16;      // 16-byte pieces of a tile
+constexpr int kRowU4 = kD / 16;            // 16-byte pieces of a token's row
+
+// Two e4m3 codes (low, high byte) to two fp16 numbers: exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(v));
+    return d;
+}
+__device__ __forceinline__ void e4m3x4_to_f16(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    lo = e4m3x2_to_f16x2((uint16_t)(v & 0xffffu));
+    hi = e4m3x2_to_f16x2((uint16_t)(v >> 16));
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// d += A (16 x 16, row) * B (16 x 8, col); fp16 operands, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The power of two that brings a row with largest magnitude amax into [2^14, 2^15), and its
+// inverse.  A bf16 query times it is an fp16 number exactly down to 2^-28 of the row's largest
+// element (below that fp16's subnormals round it, by less than 2^-39 of the largest).
+__device__ __forceinline__ float f16_row_scale(float amax, float &inverse) {
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127;       // amax >= 0; 128 for inf / NaN
+    const int k = min(14 - e, 126);                               // -114 .. 126
+    inverse = __uint_as_float((uint32_t)(127 - k) << 23);
+    return __uint_as_float((uint32_t)(127 + k) << 23);
+}
+
+// Word w (0..3) of a 16-byte piece.
+__device__ __forceinline__ uint32_t word(const uint4 &v, int w) { return w == 0 ? v.x : w == 1 ? v.y : w == 2 ? v.z : v.w; }
+
+// The lane's 8 pieces of a K tile: k[2 i + f] = piece c + 4 f of row g + 8 i.
+__device__ __forceinline__ void load_k8(uint4 (&k)[8], const uint4 *__restrict__ tile, int lane) {
+    const uint4 *src = tile + (lane >> 2) * kRowU4 + (lane & 3);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int f = 0; f < 2; ++f) k[2 * i + f] = ld_stream(src + i * 8 * kRowU4 + 4 * f);
+}
+
+// The lane's 8 pieces of a V tile: v[4 s + j] = piece g of token 16 s + 4 j + c.
+__device__ __forceinline__ void load_v8(uint4 (&v)[8], const uint4 *__restrict__ tile, int lane) {
+    const uint4 *src = tile + (lane & 3) * kRowU4 + (lane >> 2);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = ld_stream(src + x * 4 * kRowU4);
+}
+
+// Tokens at and past `visible` of a V tile loaded by load_v8 become zeros: rows behind a
+// sequence's end may hold anything, the code of NaN among it, and 0 * NaN is not 0.
+__device__ __forceinline__ void mask_v8(uint4 (&v)[8], int visible, int lane) {
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        if (4 * x + (lane & 3) >= visible) v[x] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// One decode query as the B operand of S^T = K q: column 0 holds the query, the rest zeros.
+struct Query8 {
+    uint32_t f[16];   // step (f, w): registers 2 (4 f + w), 2 (4 f + w) + 1
+    float unit;       // the products are in units of this
+};
+__device__ __forceinline__ Query8 load_query8(const uint4 *__restrict__ q_row, int lane) {
+    const int c = lane & 3;
+    float x[32];
+    float amax = 0.f;
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float y[8];
+            bf16x8_to_f32(__ldg(q_row + 8 * f + 2 * c + k), y);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                x[16 * f + 8 * k + e] = y[e];
+                amax = fmaxf(amax, fabsf(y[e]));
+            }
+        }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    Query8 q;
+    const float s = f16_row_scale(amax, q.unit);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) q.f[k] = lane < 4 ? pack_f16(x[2 * k] * s, x[2 * k + 1] * s) : 0u;
+    return q;
+}
+
+// Scores of a K tile, in units of q.unit * scale: lane (g, c) gets those of tokens g, 8 + g, 16 + g, 24 + g.
+__device__ __forceinline__ void scores8(float (&z)[4], const uint4 (&k)[8], const Query8 &q, int lane) {
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int f = 0; f < 2; ++f)
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(word(k[4 * m + f], w), a0, a2);
+                e4m3x4_to_f16(word(k[4 * m + 2 + f], w), a1, a3);
+                mma_f16(d, a0, a1, a2, a3, q.f[2 * (4 * f + w)], q.f[2 * (4 * f + w) + 1]);
+            }
+        // column 0 sits in the lanes with c = 0
+        z[2 * m] = __shfl_sync(0xffffffffu, d[0], lane & 28);
+        z[2 * m + 1] = __shfl_sync(0xffffffffu, d[2], lane & 28);
+    }
+}
+
+// acc[e] += s * sum_t p_t v[t][16 g + e] in the lanes with c = 0, for the weights p of scores8's
+// tokens.  Each weight goes to the tensor cores as the sum of two fp16 numbers, in columns 0
+// and 1 of B (which a single query leaves free): 22 bits of it are kept.
+__device__ __forceinline__ void weighted_sum8(float (&acc)[16], const float (&p)[4], const uint4 (&v)[8], float s,
+                                              int lane) {
+    const int g = lane >> 2, c = lane & 3;
+    uint32_t x01, x23;
+    {
+        const __half2 h01 = __floats2half2_rn(p[0], p[1]), h23 = __floats2half2_rn(p[2], p[3]);
+        const uint32_t l01 = pack_f16(p[0] - __low2float(h01), p[1] - __high2float(h01));
+        const uint32_t l23 = pack_f16(p[2] - __low2float(h23), p[3] - __high2float(h23));
+        x01 = c & 1 ? l01 : *reinterpret_cast<const uint32_t *>(&h01);
+        x23 = c & 1 ? l23 : *reinterpret_cast<const uint32_t *>(&h23);
+    }
+    const int src = 4 * c + (g & 1);
+    uint32_t b[2][2];
+    b[0][0] = __shfl_sync(0xffffffffu, x01, src);         // tokens c, c + 8
+    b[0][1] = __shfl_sync(0xffffffffu, x01, src + 16);    // tokens c + 4, c + 12
+    b[1][0] = __shfl_sync(0xffffffffu, x23, src);         // the same + 16
+    b[1][1] = __shfl_sync(0xffffffffu, x23, src + 16);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (g >= 2) b[k][0] = b[k][1] = 0u;
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // dims 4 w + 2 half, + 1 (rows g) and + 8 (rows g + 8)
+            float d0[4] = {0.f, 0.f, 0.f, 0.f}, d1[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t sel = half ? 0x7362u : 0x5140u;
+                uint32_t a0[2], a1[2], a2[2], a3[2];
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k], w), word(v[4 * k + 2], w), sel), a0[0], a0[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k], w + 2), word(v[4 * k + 2], w + 2), sel), a1[0], a1[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k + 1], w), word(v[4 * k + 3], w), sel), a2[0], a2[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k + 1], w + 2), word(v[4 * k + 3], w + 2), sel), a3[0], a3[1]);
+                mma_f16(d0, a0[0], a1[0], a2[0], a3[0], b[k][0], b[k][1]);
+                mma_f16(d1, a0[1], a1[1], a2[1], a3[1], b[k][0], b[k][1]);
+            }
+            const int e = 4 * w + 2 * half;
+            acc[e] = fmaf(s, d0[0] + d0[1], acc[e]);
+            acc[e + 8] = fmaf(s, d0[2] + d0[3], acc[e + 8]);
+            acc[e + 1] = fmaf(s, d1[0] + d1[1], acc[e + 1]);
+            acc[e + 9] = fmaf(s, d1[2] + d1[3], acc[e + 9]);
+        }
+    }
+}
+
+// The weight a block received, as it is added to the running totals: a weight that is not finite
+// (a query with infinities or NaN) adds nothing, so that one bad query does not spoil them.
+__device__ __forceinline__ float finite_weight(float w) { return w >= 0.f && w <= 3.4e38f ? w : 0.f; }
+
+}  // namespace uocr

@@ -473,13 +473,28 @@ prefill_block_mma_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ 
 }
 
 // ------------------------------------------------------------------ host side
-namespace {
 // Items of 16 entries: at most one partly filled item per block that was selected at all.
-size_t item_bound(int n_q, int max_blocks) {
+size_t prefill_item_bound(int n_q, int max_blocks) {
     const size_t n_entries = (size_t)n_q * kSel;
     return n_entries / kItemRows + (n_entries < (size_t)max_blocks ? n_entries : (size_t)max_blocks) + 1;
 }
-}  // namespace
+
+cudaError_t launch_prefill_invert(const LaunchCtx &c, const int32_t *counts, const int32_t *bt_row,
+                                  const int32_t *sel_ws, const int32_t *q_pos, int n_q, int max_blocks, int32_t *fill,
+                                  int4 *items, int32_t *n_items, int2 *list) {
+    const int n_entries = n_q * kSel;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.stream = c.stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;   // always after the kernel that counts the entries
+    cfg.gridDim = dim3((unsigned)((n_entries + kInvThreads * kInvEntries - 1) / (kInvThreads * kInvEntries)));
+    cfg.blockDim = dim3(kInvThreads);
+    return cudaLaunchKernelEx(&cfg, prefill_invert_kernel, counts, bt_row, sel_ws, q_pos, n_entries, max_blocks, fill,
+                              items, n_items, list);
+}
 
 size_t prefill_attn_workspace(int n_q, int H, int max_blocks, PrefillAttnWs *w) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -497,7 +512,7 @@ size_t prefill_attn_workspace(int n_q, int H, int max_blocks, PrefillAttnWs *w) 
     l.n_items_off = off;
     off += up(4);
     l.items_off = off;
-    off += up(item_bound(n_q, max_blocks) * sizeof(int4));
+    off += up(prefill_item_bound(n_q, max_blocks) * sizeof(int4));
     l.list_off = off;
     off += up((size_t)n_q * kSel * sizeof(int2));
     l.sel_off = off;     // the block kernel's entries of the selection (classified)
@@ -535,7 +550,6 @@ cudaError_t launch_prefill_attn(const LaunchCtx &c, const void *q, const void *k
     int2 *tiles = (int2 *)(base + w.tile_off);
     float *ml = (float *)(base + w.ml_off);
     __nv_bfloat16 *part_o = (__nv_bfloat16 *)(base + w.o_off);
-    const int n_entries = n_q * kSel;
 
     // classify the selection: local-window entries to the tensor-core kernel, the rest to the
     // block kernel (after a preceding kernel of the same call, or a memset)
@@ -551,10 +565,7 @@ cudaError_t launch_prefill_attn(const LaunchCtx &c, const void *q, const void *k
     cfg.attrs = attr;
     cfg.numAttrs = 1;   // every kernel here follows another kernel of the same call
 
-    cfg.gridDim = dim3((unsigned)((n_entries + kInvThreads * kInvEntries - 1) / (kInvThreads * kInvEntries)));
-    cfg.blockDim = dim3(kInvThreads);
-    e = cudaLaunchKernelEx(&cfg, prefill_invert_kernel, (const int32_t *)counts, bt_row, (const int32_t *)sel_ws,
-                           q_pos, n_entries, max_blocks, fill, items, n_items, list);
+    e = launch_prefill_invert(c, counts, bt_row, sel_ws, q_pos, n_q, max_blocks, fill, items, n_items, list);
     if (e != cudaSuccess) return e;
 
     // the local windows on tcgen05, on a few SMs beside the block kernel that follows

@@ -386,6 +386,151 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
                                         void *out, int32_t *sel_out,
                                         int32_t *dev_err, uocr_stream_t stream);
 
+/*
+ * ---- The key / value cache held in 8 bits -------------------------------------
+ *
+ * Half the bytes of the bf16 cache, in the same pages:
+ *   k_cache, v_cache   e4m3  [P][H][32][128]   one (page, head) tile = 4 KiB contiguous,
+ *                                              16-byte aligned
+ *   k_scale, v_scale   fp32  [P][H]            value = code * scale of its (page, head)
+ * Queries, outputs and the indexer cache stay bf16.  The attention takes any
+ * finite scale; the writer below makes powers of two.
+ *
+ * mass, fp32 [B][H][max_blocks], optional (NULL: not kept): running totals of
+ * the attention weight that each block received, the input of
+ * uocr_evict_blocks.  A call adds to mass[b][h][j] the softmax weights of block
+ * j's visible tokens, summed over the call's queries of sequence b; entries of
+ * blocks that were not attended are left as they are.  The order of the
+ * additions is fixed (integers where many queries meet): the same call gives the
+ * same bits.  Weights that are not finite (a query or key with infinities or
+ * NaN) add nothing.  Two calls that overlap on the GPU must not share a mass.
+ */
+
+/*
+ * uocr_rope_append over the 8-bit cache: page2d rotation of n new tokens and
+ * their append.  Sequence b's new tokens are rows new_start[b] ..
+ * new_start[b+1] - 1 of q, k_new, ... (new_start int32 [B+1], ascending from
+ * 0 to at most n; NULL: n == B and token i belongs to sequence i), at the
+ * sequence's last positions: seq_lens already counts them.  Rows past
+ * new_start[B] are not touched.
+ *   q [n][H][128], idx_q [n][128]   rotated into q_out, idx_q_out (which may be
+ *                                   q, idx_q themselves; no other overlap)
+ *   k_new, v_new [n][H][128]        rotated k and raw v, quantised
+ *   idx_k_new [n][128]              rotated, bf16, into idx_k_cache
+ * Scales, for K and V of each (page, head) that receives rows: with amax over
+ * the finite values of the rows this call adds,
+ *   need = 2^max(ceil(log2(amax / 448)), -126);
+ *   s = need, if the page holds no older row of the sequence, else
+ *       max(s_old rounded up to a power of two, need);
+ * a new value x is stored as e4m3(x / s), and where s != s_old the older rows'
+ * codes c become e4m3(c * s_old / s).  Rounding is to nearest even, once, from
+ * the value in 64 bits; infinities and NaN are stored as NaN.  Rows of the
+ * page behind the sequence's end keep what they hold.
+ * A page must not receive tokens from two sequences in one call.  A sequence
+ * whose new_start is not as above, with more new tokens than seq_lens, or
+ * longer than its table is skipped (its q rows too) and sets UOCR_DEVERR_POS; a
+ * page outside the pool is skipped (its q rows are rotated) and sets
+ * UOCR_DEVERR_PAGE.
+ */
+uocr_status_t uocr_rope_append_kv8(const void *q, const void *idx_q, const void *k_new, const void *v_new,
+                                   const void *idx_k_new, const int32_t *tok_pos, const int32_t *page_pos,
+                                   const int32_t *new_start, const int32_t *block_table, const int32_t *seq_lens,
+                                   int n, int B, int H, int max_blocks, int num_pages, void *q_out, void *idx_q_out,
+                                   void *k_cache, void *v_cache, float *k_scale, float *v_scale, void *idx_k_cache,
+                                   int32_t *dev_err, uocr_stream_t stream);
+
+/*
+ * uocr_sparse_attn over the 8-bit cache: per query i and head h,
+ *   z_t = scale * k_scale * (q[i][h] . k8[h][t])  over the tokens t <= p_i of the blocks in sel[i],
+ *   out[i][h] = sum_t softmax(z)_t * v_scale * v8[h][t]      (fp32, bf16 out).
+ * The selection, its errors and empty rows are as in uocr_sparse_attn.  Tokens
+ * behind the query's position may hold any code, NaN included.  With mass,
+ * q_seq must be NULL (one query per sequence), else UOCR_ERR_INVALID_ARG.
+ */
+uocr_status_t uocr_sparse_attn_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                   const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                   const int32_t *q_seq, const int32_t *q_pos, const int32_t *sel, int n_q, int B,
+                                   int H, int max_blocks, int num_pages, float scale, void *out, float *mass,
+                                   int32_t *dev_err, uocr_stream_t stream);
+
+/*
+ * uocr_sparse_decode over the 8-bit cache: uocr_index_score -> uocr_block_topk
+ * -> uocr_sparse_attn_kv8.  Workspace: uocr_workspace_bytes(B, H, max_blocks).
+ */
+uocr_status_t uocr_sparse_decode_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                     const float *v_scale, const void *idx_q, const void *idx_k_cache,
+                                     const int32_t *block_table, const int32_t *seq_lens, int B, int H,
+                                     int max_blocks, int num_pages, void *out, int32_t *sel_out, float *mass,
+                                     void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                     uocr_stream_t stream);
+
+/*
+ * uocr_dense_decode over the 8-bit cache: each sequence's decode query over the
+ * blocks [0, min(ref_blocks, nb)) and the local window; ref_blocks >= max_blocks
+ * is full causal attention.  Workspace: uocr_dense_kv8_workspace_bytes(B, H, max_blocks).
+ */
+size_t uocr_dense_kv8_workspace_bytes(int B, int H, int max_blocks);
+uocr_status_t uocr_dense_decode_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                    const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                    int ref_blocks, int B, int H, int max_blocks, int num_pages, void *out,
+                                    float *mass, void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                    uocr_stream_t stream);
+
+/*
+ * uocr_sparse_attn_seq over the 8-bit cache: n_q queries of sequence `seq`,
+ * each over its own selection, every selected (block, head) tile read once for
+ * all of them.  The softmax weights go to the tensor cores in fp16 and each
+ * slot's partial output is kept in fp16 (2^-12 relative each); weight sums stay
+ * fp32.  With mass, row `seq` receives the sum over the n_q queries.  Errors as
+ * uocr_sparse_attn_seq.  Workspace: uocr_sparse_attn_seq_kv8_workspace_bytes.
+ */
+size_t uocr_sparse_attn_seq_kv8_workspace_bytes(int n_q, int H, int max_blocks);
+uocr_status_t uocr_sparse_attn_seq_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                       const float *v_scale, const int32_t *block_table, const int32_t *seq_lens,
+                                       int seq, const int32_t *q_pos, const int32_t *sel, int n_q, int B, int H,
+                                       int max_blocks, int num_pages, float scale, void *out, float *mass,
+                                       void *workspace, size_t workspace_bytes, int32_t *dev_err,
+                                       uocr_stream_t stream);
+
+/*
+ * uocr_sparse_prefill over the 8-bit cache: uocr_prefill_index_score ->
+ * uocr_block_topk -> uocr_sparse_attn_seq_kv8.  Workspace:
+ * uocr_prefill_kv8_workspace_bytes (the block scores first).
+ */
+size_t uocr_prefill_kv8_workspace_bytes(int n_q, int H, int max_blocks);
+uocr_status_t uocr_sparse_prefill_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
+                                      const float *v_scale, const void *idx_q, const void *idx_k_cache,
+                                      const int32_t *block_table, const int32_t *seq_lens, int seq,
+                                      const int32_t *q_pos, int n_q, int B, int H, int max_blocks, int num_pages,
+                                      void *out, int32_t *sel_out, float *mass, void *workspace,
+                                      size_t workspace_bytes, int32_t *dev_err, uocr_stream_t stream);
+
+/*
+ * Eviction of blocks by accumulated attention weight.  A sequence of nb =
+ * ceil(seq_len / 32) blocks with nb > keep_blocks keeps its first n_sink blocks,
+ * its last 4 (the local window) and, of those between, the keep_blocks - n_sink
+ * - 4 with the highest totals sum_h mass[b][h][j] (fp64; the lower block id on
+ * ties; a NaN total ranks below every other).  The columns of the others are
+ * taken out:
+ *   new_table [B][max_blocks]      the kept columns in order, with every column at
+ *                                  nb and behind it (pages allocated ahead) moved
+ *                                  down after them, then -1
+ *   new_mass  [B][H][max_blocks]   the same of mass, then 0
+ *   new_lens  [B]                  seq_len - 32 * n_freed
+ *   freed     [B][max_blocks]      the pages of the removed columns in order, then -1
+ *   n_freed   [B]                  how many
+ * A sequence with nb <= keep_blocks is copied as it is.  Cached keys carry their
+ * rotation, so the caches are not touched; callers keep token positions for
+ * uocr_rope_append themselves.  new_mass, new_table and new_lens may be the
+ * inputs themselves; no other overlap.  keep_blocks >= n_sink + 4.  A length
+ * below 0 or beyond the table sets UOCR_DEVERR_POS and copies the sequence as it is.
+ */
+size_t uocr_evict_workspace_bytes(int B, int H, int max_blocks);
+uocr_status_t uocr_evict_blocks(const float *mass, const int32_t *block_table, const int32_t *seq_lens, int B, int H,
+                                int max_blocks, int keep_blocks, int n_sink, float *new_mass, int32_t *new_table,
+                                int32_t *new_lens, int32_t *freed, int32_t *n_freed, void *workspace,
+                                size_t workspace_bytes, int32_t *dev_err, uocr_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,662 @@
+"""The operators over the 8-bit key / value cache against plain 64-bit forms (tests/kv8_util.py, which
+also derives the bounds), through the binding."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv8_util as ref
+
+pytestmark = pytest.mark.gpu
+BLOCK = 32
+
+
+@pytest.fixture(scope="module")
+def uocr(cuda_device):
+    import block_sparse_long_uocr_b200 as m
+    return m
+
+
+def to(dev, *tensors):
+    """Copies on the device (also when it is the CPU's)."""
+    return [t.clone().to(dev) for t in tensors]
+
+
+class Case:
+    """Caches, tables and queries on the CPU; rows behind a sequence's end hold the code of NaN."""
+
+    def __init__(self, lens, H, seed, n_q=None, max_blocks=None, odd_scale=False, q_scale=1.0):
+        g = torch.Generator().manual_seed(seed)
+        self.lens, self.H, self.g = lens, H, g
+        self.mb = max_blocks or max(1, max(-(-max(x, 0) // BLOCK) for x in lens))
+        self.table, pages = ref.make_table(g, lens, self.mb)
+        self.k, self.ks = ref.make_pool(g, pages, H, odd_scale=odd_scale)
+        self.v, self.vs = ref.make_pool(g, pages, H, odd_scale=odd_scale)
+        for b, x in enumerate(lens):
+            if x > 0 and x % BLOCK:
+                for c in (self.k, self.v):
+                    c.view(torch.uint8)[int(self.table[b, x // BLOCK]), :, x % BLOCK:] = 0x7F
+        n = len(lens) if n_q is None else n_q
+        self.q = (torch.randn((n, H, 128), generator=g) * q_scale).to(torch.bfloat16)
+        self.mass = torch.rand((len(lens), H, self.mb), generator=g)
+
+    @property
+    def sl(self):
+        return torch.tensor(self.lens, dtype=torch.int32)
+
+    def select(self, positions, fill=1.0):
+        """16 slots per query: a random subset of its causal blocks, some slots empty, in any order."""
+        sel = torch.full((len(positions), 16), -1, dtype=torch.int32)
+        for i, p in enumerate(positions):
+            nb = p // BLOCK + 1 if p >= 0 else 0
+            k = min(16, nb, max(0, int(round(fill * 16))))
+            pick = torch.randperm(nb, generator=self.g)[:k] if nb else torch.empty(0, dtype=torch.long)
+            at = torch.randperm(16, generator=self.g)[:k]
+            sel[i, at] = pick.to(torch.int32)
+        return sel
+
+    def want(self, i, b, p, blocks, scale):
+        blocks = [j for j in blocks if j >= 0]
+        pages = [int(self.table[b, j]) for j in blocks]
+        return ref.attend(self.q[i], self.k, self.v, self.ks, self.vs, pages, blocks, p, scale) + (blocks,)
+
+    def gpu(self, dev):
+        return to(dev, self.q, self.k, self.v, self.ks, self.vs, self.table, self.sl)
+
+
+def check_rows(case, out, mass, rows, scale=128 ** -0.5, many=False):
+    """rows: (query, sequence, position, blocks).  mass: the GPU's totals, or None."""
+    out = out.float().cpu().double()
+    total = case.mass.double().clone()
+    bound = torch.zeros_like(total)
+    count = {}
+    for i, b, p, blocks in rows:
+        o, w, mag, vmax, used = case.want(i, b, p, blocks, scale)
+        err = (out[i] - o).abs()
+        lim = ref.out_bound(o, mag, vmax, many)
+        assert (err <= lim).all(), (i, float((err / lim).max()))
+        for x, j in enumerate(used):
+            total[b, :, j] += w[:, x]
+            bound[b, :, j] += ref.mass_bound(total[b, :, j], mag)
+        count[b] = count.get(b, 0) + 1
+    if mass is not None:
+        err = (mass.cpu().double() - total).abs()
+        assert (err <= bound).all(), float((err - bound).max())   # untouched totals: equal
+
+
+LENS = [[1], [0, 31, 32, 33], [512, 513, 511, 2000], [129, 0, 4096, 7, 700]]
+
+
+@pytest.mark.parametrize("lens", LENS)
+@pytest.mark.parametrize("H", [1, 10, 12])
+@pytest.mark.parametrize("odd_scale", [False, True])
+def test_sparse_decode_attention(uocr, cuda_device, lens, H, odd_scale):
+    c = Case(lens, H, seed=len(lens) * 100 + H, odd_scale=odd_scale)
+    pos = [x - 1 for x in lens]
+    sel = c.select(pos)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass)
+    check_rows(c, out, mass, [(i, i, pos[i], sel[i].tolist()) for i in range(len(lens))])
+    again = c.mass.to(cuda_device)
+    out2 = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=again)
+    assert torch.equal(out, out2) and torch.equal(mass, again)
+    assert torch.equal(out, uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device)))
+
+
+@pytest.mark.parametrize("fill", [0.0, 0.2, 1.0])
+def test_sparse_many_queries_per_sequence_and_scale(uocr, cuda_device, fill):
+    c = Case([700, 90, 2100], 5, seed=7, n_q=9)
+    seq = [0, 0, 1, 2, 2, 2, 1, 0, 2]
+    pos = [699, 0, 89, 31, 32, 2099, 5, 340, 1000]
+    sel = c.select(pos, fill)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), torch.tensor(seq, dtype=torch.int32, device=cuda_device),
+                               torch.tensor(pos, dtype=torch.int32, device=cuda_device), scale=0.3)
+    check_rows(c, out, None, [(i, seq[i], pos[i], sel[i].tolist()) for i in range(9)], scale=0.3)
+
+
+def test_sparse_duplicate_slots_count_twice(uocr, cuda_device):
+    c = Case([300], 3, seed=8)
+    sel = torch.tensor([[2, 9, 2, -1, 5, 2, 9, -1, -1, -1, 0, -1, -1, -1, -1, 5]], dtype=torch.int32)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass)
+    check_rows(c, out, mass, [(0, 0, 299, sel[0].tolist())])
+
+
+@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-3, 30.0, 1e20])
+def test_sparse_query_magnitudes(uocr, cuda_device, q_scale):
+    """Queries far outside fp16's range: a flat softmax for tiny ones, one token's value for huge ones."""
+    c = Case([400, 64], 4, seed=9, q_scale=q_scale)
+    sel = c.select([399, 63])
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device)).float().cpu().double()
+    for i, p in enumerate((399, 63)):
+        o, w, mag, vmax, used = c.want(i, i, p, sel[i].tolist(), 128 ** -0.5)
+        if q_scale <= 30:
+            assert ((out[i] - o).abs() <= ref.out_bound(o, mag, vmax)).all()
+        else:
+            assert torch.isfinite(out[i]).all() and (out[i].abs() <= vmax[:, None] * (1 + 2.0 ** -8)).all()
+
+
+def test_sparse_not_finite_query_stays_its_own(uocr, cuda_device):
+    c = Case([200, 300, 100], 2, seed=10)
+    c.q[1, 0, 5] = math.nan
+    c.q[1, 1, 7] = math.inf
+    sel = c.select([199, 299, 99])
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass)
+    check_rows(c, out, None, [(i, i, p, sel[i].tolist()) for i, p in ((0, 199), (2, 99))])
+    assert torch.isnan(out[1, 0].float()).all()
+    assert torch.isfinite(mass).all() and torch.equal(mass[1, 0].cpu(), c.mass[1, 0])
+
+
+def test_sparse_device_errors(uocr, cuda_device):
+    c = Case([200, 300, 100, 50], 2, seed=11)
+    sel = c.select([199, 299, 99, 49])
+    sel[0, :] = torch.tensor([7] + [-1] * 15)            # block 7 of 7 is past the end
+    c.table[1, int(sel[1][sel[1] >= 0][0])] = 10 ** 6    # outside the pool
+    bad = int(sel[1][sel[1] >= 0][0])
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    sl[3] = c.mb * BLOCK + 1
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass, dev_err=err)
+    assert int(err) == uocr.DEVERR_SEL | uocr.DEVERR_PAGE | uocr.DEVERR_POS
+    assert (out[0].float() == 0).all() and (out[3].float() == 0).all()
+    left = [j for j in sel[1].tolist() if j >= 0 and j != bad]
+    check_rows(c, out, mass, [(1, 1, 299, left), (2, 2, 99, sel[2].tolist())])
+
+
+@pytest.mark.parametrize("lens,ref_blocks", [([1], None), ([0, 31, 32, 33], None), ([2000, 513, 5000], None), ([2000, 513, 5000, 0, 90], 3),
+                                             ([1000, 64], 0), ([700, 3000], 22), ([9001], 10 ** 6)])
+@pytest.mark.parametrize("H", [1, 10])
+def test_dense_decode(uocr, cuda_device, lens, ref_blocks, H):
+    c = Case(lens, H, seed=sum(lens) + H, odd_scale=H == 1)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=ref_blocks, mass=mass)
+    rows = []
+    for b, x in enumerate(lens):
+        nb = -(-x // BLOCK)
+        rb = c.mb if ref_blocks is None else ref_blocks
+        rows.append((b, b, x - 1, [j for j in range(nb) if j < rb or j >= nb - 4]))
+    check_rows(c, out, mass, rows)
+    again = c.mass.to(cuda_device)
+    ws = torch.full((uocr.dense_kv8_workspace_bytes(len(lens), H, c.mb),), 0xFF, dtype=torch.uint8, device=cuda_device)
+    out2 = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=ref_blocks, mass=again, workspace=ws)
+    assert torch.equal(out, out2) and torch.equal(mass, again)       # whatever the workspace held
+    assert torch.equal(out, uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=ref_blocks))
+
+
+def test_dense_bad_pages_and_lengths(uocr, cuda_device):
+    c = Case([900, 400, 50], 3, seed=12)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    bt[0, 5] = -1
+    bt[0, 28] = 1 << 30
+    sl[1] = c.mb * BLOCK + 5
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, mass=mass, dev_err=err)
+    assert int(err) == uocr.DEVERR_PAGE | uocr.DEVERR_POS
+    assert (out[1].float() == 0).all()
+    check_rows(c, out, mass, [(0, 0, 899, [j for j in range(29) if j not in (5, 28)]), (2, 2, 49, [0, 1])])
+
+
+def test_a_block_of_nan_scale_or_all_minus_inf(uocr, cuda_device):
+    """A page whose scale is 0 counts as zeros; an infinite score takes the row to NaN, as the formula does."""
+    c = Case([300], 2, seed=13)
+    c.vs[int(c.table[0, 3])] = 0.0
+    c.ks[int(c.table[0, 4])] = 0.0
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl)
+    check_rows(c, out, None, [(0, 0, 299, list(range(10)))])
+
+
+@pytest.mark.parametrize("total,n,H", [(1, 1, 1), (33, 33, 3), (700, 1, 10), (700, 17, 10), (1300, 333, 4), (4100, 130, 12)])
+@pytest.mark.parametrize("order", ["chunk", "any"])
+def test_many_queries_of_a_sequence(uocr, cuda_device, total, n, H, order):
+    c = Case([total, 64], H, seed=total + n, n_q=n, odd_scale=order == "any")
+    pos = list(range(total - n, total))
+    if order == "any":
+        pos = torch.randint(0, total, (n,), generator=c.g).tolist()
+    sel = c.select(pos, 1.0 if order == "chunk" else 0.6)
+    if order == "chunk":     # the real shape: the 4 local blocks among them
+        for i, p in enumerate(pos):
+            nb = p // BLOCK + 1
+            sel[i, 12:] = -1
+            sel[i] = torch.where((sel[i] >= nb - 4), -1, sel[i])
+            sel[i, 12:] = torch.tensor([j if j >= 0 else -1 for j in range(nb - 4, nb)], dtype=torch.int32)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    qp, se = torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, qp, se, mass=mass)
+    check_rows(c, out, mass, [(i, 0, pos[i], sel[i].tolist()) for i in range(n)], many=True)
+    again = c.mass.to(cuda_device)
+    ws = torch.full((uocr.sparse_attn_seq_kv8_workspace_bytes(n, H, c.mb),), 0xFF, dtype=torch.uint8, device=cuda_device)
+    out2 = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, qp, se, mass=again, workspace=ws)
+    assert torch.equal(out, out2) and torch.equal(mass, again)
+    # and the per-query form agrees within both bounds
+    one = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, se, torch.zeros(n, dtype=torch.int32, device=cuda_device), qp)
+    check_rows(c, one, None, [(i, 0, pos[i], sel[i].tolist()) for i in range(n)])
+
+
+def test_many_queries_later_nan_does_not_reach_earlier_ones(uocr, cuda_device):
+    """A token whose value is NaN is behind some queries of its block: theirs stay finite."""
+    c = Case([160], 2, seed=14, n_q=32)
+    pos = list(range(128, 160))
+    c.v.view(torch.uint8)[int(c.table[0, 4]), 1, 20, 3] = 0xFF
+    sel = torch.full((32, 16), -1, dtype=torch.int32)
+    sel[:, :3] = torch.tensor([0, 2, 4])
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device))
+    check_rows(c, out, None, [(i, 0, pos[i], [0, 2, 4]) for i in range(20)], many=True)
+    o = out.float().cpu()
+    assert torch.isnan(o[20:, 1, 3]).all()
+    o[20:, 1, 3] = 0
+    assert torch.isfinite(o).all()
+
+
+def test_many_queries_bad_slots_positions_and_pages(uocr, cuda_device):
+    c = Case([640], 2, seed=15, n_q=6)
+    pos = [639, 700, -1, 100, 5, 300]
+    sel = c.select([639, 639, 639, 100, 5, 300], 0.5)
+    sel[3] = torch.tensor([19, 3, 1, 3, -7] + [-1] * 11)       # 19: not causal; 3 twice
+    c.table[0, 2] = -5
+    sel[5] = torch.tensor([2, 4] + [-1] * 14)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device),
+                                   mass=mass, dev_err=err)
+    assert int(err) == uocr.DEVERR_SEL | uocr.DEVERR_PAGE | uocr.DEVERR_POS
+    assert (out[1:3].float() == 0).all()
+    fine = lambda i: [j for j in sel[i].tolist() if 0 <= j <= pos[i] // BLOCK and j != 2]  # noqa: E731
+    check_rows(c, out, mass, [(i, 0, pos[i], fine(i)) for i in (0, 3, 4, 5)], many=True)
+
+
+# ------------------------------------------------------------------------------------------ append
+def append_state(seed, H, lens, new, extra_rows=0, spare=3):
+    g = torch.Generator().manual_seed(seed)
+    mb = max(1, max(-(-x // BLOCK) for x in lens))
+    table, pages = ref.make_table(g, lens, mb, spare)
+    n = sum(new) + extra_rows
+    s = {}
+    s["k"], s["k_scale"] = ref.make_pool(g, pages, H)
+    s["v"], s["v_scale"] = ref.make_pool(g, pages, H)
+    for name, shape in (("q", (n, H, 128)), ("idx_q", (n, 128)), ("k_new", (n, H, 128)), ("v_new", (n, H, 128)), ("idx_k_new", (n, 128)),
+                        ("idx_k", (pages, BLOCK, 128))):
+        s[name] = torch.randn(shape, generator=g).to(torch.bfloat16)
+    for name in ("k_new", "v_new"):      # some raise their page's scale, some do not
+        s[name] *= torch.exp(1.2 * torch.randn((n, H, 1), generator=g)).to(torch.bfloat16)
+    s["tok"] = torch.randint(0, 120000, (n,), generator=g, dtype=torch.int32)
+    s["page"] = torch.randint(-3, 50, (n,), generator=g, dtype=torch.int32)
+    starts = [0]
+    for x in new:
+        starts.append(starts[-1] + x)
+    return s, table, starts, n
+
+
+def run_append(uocr, dev, s, table, lens, starts, in_place=False, dev_err=None, null_start=False):
+    d = {k: v.clone().to(dev) for k, v in s.items()}
+    bt, sl = table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+    q_out = None if in_place else torch.full_like(d["q"], 7.0)
+    i_out = None if in_place else torch.full_like(d["idx_q"], 7.0)
+    st = None if null_start else torch.tensor(starts, dtype=torch.int32, device=dev)
+    q, i = uocr.rope_append_kv8(d["q"], d["idx_q"], d["k_new"], d["v_new"], d["idx_k_new"], d["tok"], d["page"], bt, sl, d["k"], d["v"],
+                                d["k_scale"], d["v_scale"], d["idx_k"], st, q_out=q_out, idx_q_out=i_out, dev_err=dev_err)
+    torch.cuda.synchronize()
+    assert (q.data_ptr() == d["q"].data_ptr()) == in_place
+    return q, i, {k: d[k].cpu() for k in ("k", "v", "k_scale", "v_scale", "idx_k")}
+
+
+def same_codes(a, b):
+    """Codes equal, NaN in either sign."""
+    a, b = a.view(torch.uint8).numpy(), b
+    return bool(((a == b) | ((a & 127 == 127) & (b & 127 == 127))).all())
+
+
+def check_append(s, got, want, old_q):
+    q, i, caches = got
+    for name in ("k", "v"):
+        assert same_codes(caches[name], want[name]), name
+        assert np.array_equal(caches[name + "_scale"].double().numpy(), want[name + "_scale"]), name
+    for t, w, old in ((q, want["q"], old_q[0]), (i, want["idx_q"], old_q[1])):
+        t = t.float().cpu().double().numpy()
+        put = np.isfinite(w)
+        assert (np.abs(t - w)[put] <= np.abs(w[put]) * 2.0 ** -8 + 1e-38).all()
+        assert np.array_equal(t[~put], old.double().numpy()[~put])            # rows that belong to no sequence
+    k, w = caches["idx_k"].double().numpy(), want["idx_k"]
+    assert (np.abs(k - w) <= np.where(want["wrote"][..., None], np.abs(w) * 2.0 ** -8 + 1e-38, 0)).all()
+
+
+@pytest.mark.parametrize("lens,new", [([1], [1]), ([32, 33, 64, 5], [1, 1, 1, 1]), ([100], [100]), ([77, 5, 200], [40, 5, 70]),
+                                      ([300, 31, 64, 96, 1], [257, 0, 32, 33, 1]), ([33, 65], [2, 34]), ([700], [1])])
+@pytest.mark.parametrize("H", [1, 10])
+def test_append(uocr, cuda_device, lens, new, H):
+    s, table, starts, n = append_state(sum(lens) + H, H, lens, new, extra_rows=2)
+    want = ref.append(s, starts, lens, table)
+    got = run_append(uocr, cuda_device, s, table, lens, starts)
+    check_append(s, got, want, (torch.full_like(s["q"], 7.0), torch.full_like(s["idx_q"], 7.0)))
+    place = run_append(uocr, cuda_device, s, table, lens, starts, in_place=True)
+    check_append(s, place, want, (s["q"], s["idx_q"]))
+    if new == [1] * len(lens):
+        s2 = {k: (v[:n - 2] if v.shape[0] == n and k not in ("k", "v", "k_scale", "v_scale", "idx_k") else v) for k, v in s.items()}
+        one = run_append(uocr, cuda_device, s2, table, lens, starts, null_start=True)
+        for k in ("k", "v"):
+            assert same_codes(one[2][k], want[k])
+
+
+def test_append_is_the_same_in_any_chunks(uocr, cuda_device):
+    """One chunk of 90 tokens, or the same 90 in calls of one: equal values wherever the scale did not need a second
+    rounding, and equal scales."""
+    H, lens = 3, [90]
+    s, table, starts, n = append_state(5, H, lens, [90])
+    _, _, whole = run_append(uocr, cuda_device, s, table, lens, starts)
+    dev = cuda_device
+    d = {k: v.clone().to(dev) for k, v in s.items()}
+    bt = table.to(dev)
+    for i in range(90):
+        sl = torch.tensor([i + 1], dtype=torch.int32, device=dev)
+        uocr.rope_append_kv8(*[d[x][i:i + 1].clone() for x in ("q", "idx_q", "k_new", "v_new", "idx_k_new", "tok", "page")], bt, sl,
+                             d["k"], d["v"], d["k_scale"], d["v_scale"], d["idx_k"])
+    for x in "kv":
+        used = [int(p) for p in table[0]]
+        a, b = whole[x + "_scale"][used], d[x + "_scale"].cpu()[used]
+        assert torch.equal(a, b)
+        va, vb = ref.values(whole[x])[used], ref.values(d[x])[used]
+        rows = torch.arange(3 * BLOCK).reshape(3, 1, BLOCK, 1) < 90
+        # below e4m3's normal range (2^-6) a code may have been rounded twice: by at most a step of 2^-9
+        diff = torch.where(rows, (va - vb).abs(), 0.0)
+        assert (diff <= torch.where(va.abs() < 2.0 ** -5, 2.0 ** -9, 0.0)).all()
+    assert torch.equal(whole["idx_k"], d["idx_k"].cpu())
+
+
+def test_append_extreme_values(uocr, cuda_device):
+    lens, H = [40, 64], 2
+    s, table, starts, n = append_state(6, H, lens, [20, 64])
+    s["k_new"][3] = 0
+    s["v_new"][:20] = 0                       # an older page, all new rows zero
+    s["v_new"][20:52, 1] = 0                  # a fresh page of zeros: the least scale
+    s["v_new"][60, 0, 5] = math.nan
+    s["v_new"][61, 0, 6] = math.inf
+    s["v_new"][62, 0, 7] = -math.inf
+    s["v_new"][63, 1] = 1e38
+    s["k_new"][70, 0] = 3e38
+    s["k_new"][71, 1] = 1e-40
+    s["k_scale"][int(table[0, 0])] = 0.013    # not a power of two
+    want = ref.append(s, starts, lens, table)
+    got = run_append(uocr, cuda_device, s, table, lens, starts)
+    check_append(s, got, want, (torch.full_like(s["q"], 7.0), torch.full_like(s["idx_q"], 7.0)))
+
+
+def test_append_bad_sequences_are_skipped(uocr, cuda_device):
+    lens = [40, 5, 96, 70]
+    s, table, starts, n = append_state(7, 2, lens, [10, 5, 40, 3])
+    lens[1] = 4                                  # more new tokens than the sequence has
+    table[2, 2] = 10 ** 7                        # a page outside the pool: its q rows are still rotated
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    want = ref.append(s, starts, lens, table)
+    got = run_append(uocr, cuda_device, s, table, lens, starts, dev_err=err)
+    assert int(err) == uocr.DEVERR_POS | uocr.DEVERR_PAGE
+    check_append(s, got, want, (torch.full_like(s["q"], 7.0), torch.full_like(s["idx_q"], 7.0)))
+
+
+@pytest.mark.parametrize("starts", [[0, 12, 5, 20], [-4, 3, 9, 20], [0, 8, 16, 999], [9, 9, 9, 9]])
+def test_append_starts_out_of_order_stay_in_bounds(uocr, cuda_device, starts):
+    """Starts that do not ascend from 0 to n: what is not a sequence's own rows is skipped and flagged."""
+    lens = [40, 50, 60]
+    s, table, _, n = append_state(8, 1, lens, [7, 7, 6])
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    run_append(uocr, cuda_device, s, table, lens, starts, dev_err=err)
+    assert int(err) == (0 if starts == [9, 9, 9, 9] else uocr.DEVERR_POS)
+
+
+# ---------------------------------------------------------------------------------------- eviction
+def run_evict(uocr, dev, mass, table, lens, keep, sink, in_place=False):
+    m, t, n = to(dev, mass, table, lens)
+    err = torch.zeros(1, dtype=torch.int32, device=dev)
+    kw = dict(new_mass=m, new_table=t, new_lens=n) if in_place else {}
+    r = uocr.evict_blocks(m, t, n, keep, n_sink=sink, dev_err=err, **kw)
+    return [x.cpu() for x in r], int(err)
+
+
+@pytest.mark.parametrize("mb,H", [(1, 1), (9, 3), (33, 10), (1024, 2), (1025, 5), (5000, 3)])
+@pytest.mark.parametrize("kind", ["long_tail", "ties", "zeros", "odd_values"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict(uocr, cuda_device, mb, H, kind, in_place):
+    g = torch.Generator().manual_seed(mb * 7 + H)
+    B = 5
+    mass = torch.exp(2 * torch.randn((B, H, mb), generator=g))
+    if kind == "ties":
+        mass = torch.randint(0, 3, (B, H, mb), generator=g).float()
+    elif kind == "zeros":
+        mass[torch.rand((B, 1, mb), generator=g).expand(B, H, mb) < 0.9] = 0.0
+    elif kind == "odd_values":
+        mass[torch.rand(mass.shape, generator=g) < 0.1] *= -1
+        mass[torch.rand(mass.shape, generator=g) < 0.02] = math.nan
+        mass[:, 0][torch.rand((B, mb), generator=g) < 0.02] = math.inf
+        mass[torch.rand(mass.shape, generator=g) < 0.1] = -0.0
+    table = torch.randint(0, 1 << 20, (B, mb), generator=g, dtype=torch.int32)
+    lens = torch.tensor([mb * BLOCK, 0, max(1, mb * BLOCK - 17), mb * BLOCK // 2 + 1, 1], dtype=torch.int32)
+    for keep, sink in ((4, 0), (5, 1), (max(6, mb // 3), 2), (mb + 4, 0)):
+        if sink > mb:
+            continue
+        want = ref.evict(mass, table, lens, keep, sink)
+        got, err = run_evict(uocr, cuda_device, mass, table, lens, keep, sink, in_place)
+        assert err == 0
+        for w, x, name in zip(want, got, ("mass", "table", "lens", "freed", "n_freed")):
+            assert torch.equal(w.view(torch.int32) if w.is_floating_point() else w, x.view(torch.int32) if x.is_floating_point() else x), (name, keep, sink)
+
+
+def test_evict_bad_lengths_copy_and_flag(uocr, cuda_device):
+    mass, table = torch.rand((3, 2, 50)), torch.arange(150, dtype=torch.int32).reshape(3, 50)
+    lens = torch.tensor([-1, 50 * BLOCK + 1, 1000], dtype=torch.int32)
+    got, err = run_evict(uocr, cuda_device, mass, table, lens, 10, 0)
+    assert err == uocr.DEVERR_POS
+    for w, x in zip(ref.evict(mass, table, lens, 10, 0), got):
+        assert torch.equal(w, x)
+
+
+# --------------------------------------------------------------------- streams, graphs, used together
+def test_binding_refusals(uocr, cuda_device):
+    c = Case([300, 64], 2, seed=20)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    sel = c.select([299, 63]).to(cuda_device)
+    mass = c.mass.to(cuda_device)
+    seq = torch.zeros(2, dtype=torch.int32, device=cuda_device)
+    for bad in (dict(k_cache=k.view(torch.uint8)), dict(k_scale=ks[:-1].contiguous()), dict(k_scale=ks.double()), dict(v_cache=v[1:].contiguous()),
+                dict(sel=sel[:, :15].contiguous()), dict(sel=sel.long()), dict(mass=mass[:, :, :-1].contiguous()), dict(mass=mass, q_seq=seq),
+                dict(out=q[:1]), dict(q=q.transpose(0, 1)), dict(seq_lens=sl[:1]), dict(block_table=bt.long()), dict(q_pos=seq[:1]),
+                dict(v_scale=vs.cpu()), dict(dev_err=torch.zeros(1, device=cuda_device)), dict(scale=math.nan)):
+        a = dict(q=q, k_cache=k, v_cache=v, k_scale=ks, v_scale=vs, block_table=bt, seq_lens=sl, sel=sel)
+        a.update(bad)
+        with pytest.raises((ValueError, TypeError, uocr.UocrError)):
+            uocr.sparse_attn_kv8(**a)
+    with pytest.raises(uocr.UocrError):
+        uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=-1)
+    with pytest.raises(uocr.UocrError):
+        uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, workspace=torch.empty(256, dtype=torch.uint8, device=cuda_device))
+    with pytest.raises(uocr.UocrError):
+        uocr.evict_blocks(mass, bt, sl, 3)
+    with pytest.raises(uocr.UocrError):
+        uocr.evict_blocks(mass, bt, sl, 8, new_table=bt, freed=bt)
+    with pytest.raises(uocr.UocrError):
+        uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 2, seq, sel)
+    assert uocr.sparse_attn_seq_kv8(q[:0], k, v, ks, vs, bt, sl, 0, seq[:0], sel[:0]).shape == (0, 2, 128)
+
+
+def test_matches_the_bf16_cache_of_the_same_values(uocr, cuda_device):
+    """Power-of-two scales make every cached value a bf16 number, so both caches hold the same keys and values."""
+    c = Case([700, 1500, 90], 10, seed=21)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    kb = (k.float() * ks[:, :, None, None]).nan_to_num(0).to(torch.bfloat16)
+    vb = (v.float() * vs[:, :, None, None]).nan_to_num(0).to(torch.bfloat16)
+    g = torch.Generator().manual_seed(3)
+    iq = torch.randn((3, 128), generator=g).to(torch.bfloat16).to(cuda_device)
+    ik = torch.randn((k.shape[0], 32, 128), generator=g).to(torch.bfloat16).to(cuda_device)
+    o8, s8 = uocr.sparse_decode_kv8(q, k, v, ks, vs, iq, ik, bt, sl)
+    o16, s16 = uocr.sparse_decode(q, kb, vb, iq, ik, bt, sl)
+    assert torch.equal(s8, s16)
+    check_rows(c, o8, None, [(i, i, c.lens[i] - 1, s8[i].tolist()) for i in range(3)])
+    assert (o8.float() - o16.float()).abs().max() <= 2.0 ** -7 * o16.float().abs().max()
+
+
+def test_prefill_step_selects_like_the_bf16_one(uocr, cuda_device):
+    n, total = 70, 2100
+    c = Case([total], 3, seed=22, n_q=n)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    g = torch.Generator().manual_seed(4)
+    iq = torch.randn((n, 128), generator=g).to(torch.bfloat16).to(cuda_device)
+    ik = torch.randn((k.shape[0], 32, 128), generator=g).to(torch.bfloat16).to(cuda_device)
+    pos = torch.arange(total - n, total, dtype=torch.int32, device=cuda_device)
+    mass = c.mass.to(cuda_device)
+    out, sel = uocr.sparse_prefill_kv8(q, k, v, ks, vs, iq, ik, bt, sl, 0, pos, mass=mass)
+    zero = torch.zeros((k.shape[0], 3, 32, 128), dtype=torch.bfloat16, device=cuda_device)
+    _, want = uocr.sparse_prefill(q, zero, zero, iq, ik, bt, sl, 0, pos)
+    assert torch.equal(sel, want)
+    sel = sel.cpu()
+    check_rows(c, out, mass, [(i, 0, total - n + i, sel[i].tolist()) for i in range(n)], many=True)
+
+
+def test_captured_replayed_and_on_another_stream(uocr, cuda_device):
+    """A decode step (append, attention with totals, eviction) captured once and replayed on new contents, beside a
+    second graph that shares the first one's workspace."""
+    lens, H = [500, 1000], 3
+    s, table, starts, n = append_state(30, H, lens, [1, 1])
+    d = {k: v.to(cuda_device) for k, v in s.items()}
+    bt, sl = table.to(cuda_device), torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+    mb = table.shape[1]
+    mass = torch.zeros((2, H, mb), device=cuda_device)
+    ws = torch.empty(uocr.dense_kv8_workspace_bytes(2, H, mb), dtype=torch.uint8, device=cuda_device)
+    ews = torch.empty(uocr.evict_workspace_bytes(2, H, mb), dtype=torch.uint8, device=cuda_device)
+    qo, io = torch.empty_like(d["q"]), torch.empty_like(d["idx_q"])
+    out, ev = torch.empty_like(d["q"]), [torch.empty_like(mass), torch.empty_like(bt), torch.empty_like(sl), torch.empty_like(bt), torch.empty_like(sl)]
+
+    def step():
+        uocr.rope_append_kv8(d["q"], d["idx_q"], d["k_new"], d["v_new"], d["idx_k_new"], d["tok"], d["page"], bt, sl, d["k"], d["v"],
+                             d["k_scale"], d["v_scale"], d["idx_k"], q_out=qo, idx_q_out=io)
+        uocr.dense_decode_kv8(qo, d["k"], d["v"], d["k_scale"], d["v_scale"], bt, sl, out=out, mass=mass, workspace=ws)
+        uocr.evict_blocks(mass, bt, sl, 12, n_sink=1, new_mass=ev[0], new_table=ev[1], new_lens=ev[2], freed=ev[3], n_freed=ev[4], workspace=ews)
+
+    start = {k: v.clone() for k, v in d.items()}
+
+    def reset():
+        for k, v in start.items():
+            d[k].copy_(v)
+        mass.zero_()
+
+    step()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (out, mass, *ev)]
+    reset()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    for a, b in zip(want, (out, mass, *ev)):
+        assert torch.equal(a, b)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        graphs.append(g)
+    for g in (graphs[0], graphs[1], graphs[0]):
+        reset()
+        for x in (out, *ev):
+            x.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(want, (out, mass, *ev)):
+            assert torch.equal(a, b)
+
+
+def test_prompt_decode_evict_decode(uocr, cuda_device):
+    """The operators as a server uses them: a prompt appended and attended in two chunks, decode steps, an eviction in
+    place, pages freed, more decode steps on the shorter table; every attention against the 64-bit form on the cache
+    as it stands, every total and every table against the plain ones."""
+    dev, H, keep, sink = cuda_device, 4, 14, 1
+    g = torch.Generator().manual_seed(40)
+    mb, pages = 40, 60
+    rnd = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16)  # noqa: E731
+    c = Case([0, 0], H, seed=41, max_blocks=mb)      # holder of the caches on the CPU side
+    c.k = torch.full((pages, H, 32, 128), math.nan).to(torch.float8_e4m3fn)
+    c.v, c.ks, c.vs = c.k.clone(), torch.full((pages, H), math.nan), torch.full((pages, H), math.nan)
+    k, v, ks, vs = to(dev, c.k, c.v, c.ks, c.vs)
+    ik = torch.zeros((pages, 32, 128), dtype=torch.bfloat16, device=dev)
+    free = torch.randperm(pages, generator=g).tolist()
+    table = torch.full((2, mb), -1, dtype=torch.int32)
+    lens, true_pos = [0, 0], [0, 0]
+    mass = torch.zeros((2, H, mb), device=dev)
+    c.mass = torch.zeros((2, H, mb))
+
+    def grow(b, n):
+        for j in range(-(-lens[b] // 32), -(-(lens[b] + n) // 32)):
+            table[b, j] = free.pop()
+        lens[b] += n
+
+    def mirror():
+        c.k, c.v, c.ks, c.vs = [x.cpu() for x in (k, v, ks, vs)]
+        c.table = table
+
+    def append(news):
+        for b, n in enumerate(news):
+            grow(b, n)
+        n = sum(news)
+        q, iq, kn, vn, ikn = rnd(n, H, 128), rnd(n, 128), rnd(n, H, 128), rnd(n, H, 128), rnd(n, 128)
+        tok = torch.cat([torch.arange(true_pos[b], true_pos[b] + m, dtype=torch.int32) for b, m in enumerate(news)])
+        for b, m in enumerate(news):
+            true_pos[b] += m
+        st = torch.tensor([0, news[0], n], dtype=torch.int32, device=dev)
+        q, iq, kn, vn, ikn, tok = [x.to(dev) for x in (q, iq, kn, vn, ikn, tok)]
+        bt, sl = table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+        uocr.rope_append_kv8(q, iq, kn, vn, ikn, tok, torch.zeros_like(tok), bt, sl, k, v, ks, vs, ik, st)
+        return q, iq, bt, sl
+
+    for news in ([150, 33], [300, 77]):
+        q, iq, bt, sl = append(news)
+        mirror()
+        c.q = q.cpu()
+        at = 0
+        for b, n in enumerate(news):
+            pos = torch.arange(lens[b] - n, lens[b], dtype=torch.int32, device=dev)
+            out, sel = uocr.sparse_prefill_kv8(q[at:at + n], k, v, ks, vs, iq[at:at + n], ik, bt, sl, b, pos, mass=mass)
+            full = torch.zeros_like(c.q)
+            full[at:at + n] = out.cpu()
+            check_rows(c, full, mass, [(at + i, b, int(pos[i]), sel[i].tolist()) for i in range(n)], many=True)
+            c.mass = mass.cpu()
+            at += n
+
+    def decode(steps):
+        for x in range(steps):
+            q, iq, bt, sl = append([1, 1])
+            mirror()
+            c.q = q.cpu()
+            if x % 2:
+                out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, mass=mass)
+                rows = [(b, b, lens[b] - 1, list(range(-(-lens[b] // 32)))) for b in range(2)]
+            else:
+                out, sel = uocr.sparse_decode_kv8(q, k, v, ks, vs, iq, ik, bt, sl, mass=mass)
+                rows = [(b, b, lens[b] - 1, sel[b].tolist()) for b in range(2)]
+            check_rows(c, out, mass, rows)
+            c.mass = mass.cpu()
+
+    decode(5)
+    bt, sl = table.to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+    want = ref.evict(mass.cpu(), table, torch.tensor(lens, dtype=torch.int32), keep, sink)
+    got = uocr.evict_blocks(mass, bt, sl, keep, n_sink=sink, new_mass=mass, new_table=bt, new_lens=sl)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b.cpu())
+    assert got[4].tolist() == [1, 0] or got[4][0] > 0
+    for b in range(2):
+        free += [int(x) for x in got[3][b, :int(got[4][b])]]
+    table.copy_(bt.cpu())
+    lens[:] = sl.tolist()
+    c.mass = mass.cpu()
+    assert -(-lens[0] // 32) == keep
+    decode(4)
