@@ -608,64 +608,86 @@ def evict_workspace_bytes(n_seq: int, heads: int, max_blocks: int) -> int:
     return int(_lib().uocr_evict_workspace_bytes(int(n_seq), int(heads), int(max_blocks)))
 
 
-def _one_device(*tensors):
-    """The device of all the given tensors (None among them is skipped)."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
-    return dev
+# The entry points below check their tensors on every call of a decode loop: `_fits` asks the four
+# things that matter as cheaply as Python can, and only when one is wrong does `_refuse` look for it
+# and say which (28 us per call of sparse_attn_kv8, its launch included, became 12.5).
+_BF16, _F32, _I32, _E4M3, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
 
 
-def _launch(fn: str, dev, stream, *args):
-    """Call uocr_<fn>(*args, stream) with `dev` current, on its current stream unless one is given."""
-    with torch.cuda.device(dev):
-        s = torch.cuda.current_stream(dev) if stream is None else stream
-        _check("uocr_" + fn, getattr(_lib(), "uocr_" + fn)(*args, ctypes.c_void_p(s.cuda_stream)))
+def _fits(t, dtype, shape, dev: int) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _workspace(workspace, nbytes: int, dev) -> torch.Tensor:
+def _refuse(dev: int, *specs):
+    """Raise for the first of (tensor, name, dtype, shape) that does not fit device `dev`; None tensors are skipped."""
+    for t, name, dtype, shape in specs:
+        if t is None:
+            continue
+        _dev(t, name, dtype, len(shape))
+        _shape(t, name, shape)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} must be on cuda:{dev} like the other tensors, got {t.device}")
+
+
+def _device_of(t, name: str, dtype, ndim: int) -> int:
+    """The device index of a call's leading tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or not t.is_contiguous():
+        _dev(t, name, dtype, ndim)
+    return t.get_device()
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _launch(fn, name: str, dev: int, stream, *args):
+    """fn(*args, stream) with device `dev` current, on its current stream unless one is given."""
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        raw = stream.cuda_stream
+        if stream.device.index != dev:
+            raise ValueError(f"stream must be on cuda:{dev} like the tensors, got {stream.device}")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, raw)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, raw)
+    if st != 0:
+        _check("uocr_" + name, st)
+
+
+def _kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H):
+    return ((k_cache, "k_cache", _E4M3, (P, H, BLOCK, HEAD_DIM)), (v_cache, "v_cache", _E4M3, (P, H, BLOCK, HEAD_DIM)),
+            (k_scale, "k_scale", _F32, (P, H)), (v_scale, "v_scale", _F32, (P, H)))
+
+
+def _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev) -> bool:
+    tile, scale = (P, H, BLOCK, HEAD_DIM), (P, H)
+    return (_fits(k_cache, _E4M3, tile, dev) and _fits(v_cache, _E4M3, tile, dev) and _fits(k_scale, _F32, scale, dev)
+            and _fits(v_scale, _F32, scale, dev))
+
+
+def _pool(k_cache):
+    _device_of(k_cache, "k_cache", _E4M3, 4)
+    return k_cache.shape[0]
+
+
+def _space(workspace, nbytes, dev: int):
+    """The caller's workspace, or a new one of nbytes() bytes on device `dev`."""
     if workspace is None:
-        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=dev)
-    return _dev(workspace, "workspace", torch.uint8, 1)
+        return torch.empty(max(nbytes(), 1), dtype=_U8, device=torch.device("cuda", dev))
+    if workspace.dim() != 1 or not _fits(workspace, _U8, workspace.shape, dev):
+        _refuse(dev, (workspace, "workspace", _U8, (None,)))
+    return workspace
 
 
-def _check_kv8(k_cache, v_cache, k_scale, v_scale, H):
-    """e4m3 caches [P, H, 32, 128] and their fp32 scales [P, H]."""
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _dev(t, n, torch.float8_e4m3fn, 4)
-    _check_caches(k_cache, v_cache, H)
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _dev(t, n, torch.float32, 2)
-        _shape(t, n, (k_cache.shape[0], H))
-
-
-def _check_seqs(block_table, seq_lens, B=None):
-    _dev(block_table, "block_table", torch.int32, 2)
-    _dev(seq_lens, "seq_lens", torch.int32, 1)
-    _shape(block_table, "block_table", (B, None))
-    _shape(seq_lens, "seq_lens", (block_table.shape[0],))
-
-
-def _check_mass(mass, B, H, mb):
-    if mass is not None:
-        _dev(mass, "mass", torch.float32, 3)
-        _shape(mass, "mass", (B, H, mb))
-
-
-def _out(out, q):
-    if out is None:
-        return torch.empty_like(q)
-    _dev(out, "out", torch.bfloat16, 3)
-    return _shape(out, "out", tuple(q.shape))
-
-
-def _dev_err(dev_err):
-    if dev_err is not None:
-        _dev(dev_err, "dev_err", torch.int32)
-        if dev_err.numel() < 1:
-            raise ValueError("dev_err must hold one int32")
-    return dev_err
+def _check_dev_err(dev_err, dev: int):
+    if dev_err is None:
+        return
+    if dev_err.numel() < 1 or not _fits(dev_err, _I32, dev_err.shape, dev):
+        _dev(dev_err, "dev_err", _I32)
+        raise ValueError(f"dev_err must hold one int32 on cuda:{dev}")
 
 
 def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_table, seq_lens, k_cache, v_cache,
@@ -675,87 +697,114 @@ def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_
     and raw v quantised to e4m3 under one power-of-two scale per (page, head), rotated idx_k as bf16.  Sequence b's
     new tokens are rows new_start[b] .. new_start[b + 1] - 1 (None: token i belongs to sequence i) and take the
     sequence's last positions.  Returns (q_out, idx_q_out)."""
-    for t, n, dt, nd in ((q, "q", torch.bfloat16, 3), (idx_q, "idx_q", torch.bfloat16, 2),
-                         (k_new, "k_new", torch.bfloat16, 3), (v_new, "v_new", torch.bfloat16, 3),
-                         (idx_k_new, "idx_k_new", torch.bfloat16, 2), (tok_pos, "tok_pos", torch.int32, 1),
-                         (page_pos, "page_pos", torch.int32, 1), (idx_k_cache, "idx_k_cache", torch.bfloat16, 3)):
-        _dev(t, n, dt, nd)
-    n, H = q.shape[0], q.shape[1]
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens)
+    dev = _device_of(q, "q", _BF16, 3)
+    n, H, _ = q.shape
+    P = _pool(k_cache)
+    _device_of(block_table, "block_table", _I32, 2)
     B, mb = block_table.shape
-    _shape(q, "q", (n, H, HEAD_DIM))
-    _shape(idx_q, "idx_q", (n, IDX_DIM))
-    _shape(k_new, "k_new", (n, H, HEAD_DIM))
-    _shape(v_new, "v_new", (n, H, HEAD_DIM))
-    _shape(idx_k_new, "idx_k_new", (n, IDX_DIM))
-    _shape(tok_pos, "tok_pos", (n,))
-    _shape(page_pos, "page_pos", (n,))
-    _shape(idx_k_cache, "idx_k_cache", (k_cache.shape[0], BLOCK, IDX_DIM))
-    _opt_i32(new_start, "new_start", B + 1)
-    q_out = q if q_out is None else _out(q_out, q)
+    if q_out is None:
+        q_out = q
     if idx_q_out is None:
         idx_q_out = idx_q
-    _dev(idx_q_out, "idx_q_out", torch.bfloat16, 2)
-    _shape(idx_q_out, "idx_q_out", (n, IDX_DIM))
-    dev = _one_device(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_table, seq_lens, k_cache, v_cache,
-                      k_scale, v_scale, idx_k_cache, new_start, q_out, idx_q_out, _dev_err(dev_err))
-    _launch("rope_append_kv8", dev, stream, _ptr(q), _ptr(idx_q), _ptr(k_new), _ptr(v_new), _ptr(idx_k_new),
-            _ptr(tok_pos), _ptr(page_pos), _ptr(new_start), _ptr(block_table), _ptr(seq_lens), n, B, H, mb,
-            k_cache.shape[0], _ptr(q_out), _ptr(idx_q_out), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-            _ptr(v_scale), _ptr(idx_k_cache), _ptr(dev_err))
+    heads, idx = (n, H, HEAD_DIM), (n, IDX_DIM)
+    try:
+        good = (_fits(q, _BF16, heads, dev) and _fits(idx_q, _BF16, idx, dev) and _fits(k_new, _BF16, heads, dev)
+                and _fits(v_new, _BF16, heads, dev) and _fits(idx_k_new, _BF16, idx, dev)
+                and _fits(tok_pos, _I32, (n,), dev) and _fits(page_pos, _I32, (n,), dev)
+                and _fits(block_table, _I32, (B, mb), dev) and _fits(seq_lens, _I32, (B,), dev)
+                and _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev)
+                and _fits(idx_k_cache, _BF16, (P, BLOCK, IDX_DIM), dev)
+                and (new_start is None or _fits(new_start, _I32, (B + 1,), dev))
+                and (q_out is q or _fits(q_out, _BF16, heads, dev))
+                and (idx_q_out is idx_q or _fits(idx_q_out, _BF16, idx, dev)))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(dev, (q, "q", _BF16, heads), (idx_q, "idx_q", _BF16, idx), (k_new, "k_new", _BF16, heads),
+                (v_new, "v_new", _BF16, heads), (idx_k_new, "idx_k_new", _BF16, idx), (tok_pos, "tok_pos", _I32, (n,)),
+                (page_pos, "page_pos", _I32, (n,)), (block_table, "block_table", _I32, (B, mb)),
+                (seq_lens, "seq_lens", _I32, (B,)), *_kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H),
+                (idx_k_cache, "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)), (new_start, "new_start", _I32, (B + 1,)),
+                (q_out, "q_out", _BF16, heads), (idx_q_out, "idx_q_out", _BF16, idx))
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_rope_append_kv8, "rope_append_kv8", dev, stream, q.data_ptr(), idx_q.data_ptr(),
+            k_new.data_ptr(), v_new.data_ptr(), idx_k_new.data_ptr(), tok_pos.data_ptr(), page_pos.data_ptr(),
+            _at(new_start), block_table.data_ptr(), seq_lens.data_ptr(), n, B, H, mb, P, q_out.data_ptr(),
+            idx_q_out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            idx_k_cache.data_ptr(), _at(dev_err))
     return q_out, idx_q_out
+
+
+def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_seq, out, mass, more=()):
+    """The checks that the attention entry points share; `more`: their other (tensor, name, dtype, shape), which may
+    be None.  n_seq: what the table's first extent must be (None: any).  Returns (device, n, H, P, B, max_blocks, out)."""
+    dev = _device_of(q, "q", _BF16, 3)
+    n, H, _ = q.shape
+    P = _pool(k_cache)
+    _device_of(block_table, "block_table", _I32, 2)
+    B, mb = block_table.shape
+    rows = (n, H, HEAD_DIM)
+    if out is None:
+        out = torch.empty_like(q)
+    try:
+        good = (q.shape[2] == HEAD_DIM and (n_seq is None or n_seq == B) and block_table.get_device() == dev
+                and _fits(seq_lens, _I32, (B,), dev) and _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev)
+                and _fits(out, _BF16, rows, dev) and (mass is None or _fits(mass, _F32, (B, H, mb), dev)))
+        for t, _, dtype, shape in more:
+            good = good and (t is None or _fits(t, dtype, shape, dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(dev, (q, "q", _BF16, rows), (block_table, "block_table", _I32, (B if n_seq is None else n_seq, mb)),
+                (seq_lens, "seq_lens", _I32, (B,)), *_kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H),
+                (out, "out", _BF16, rows), (mass, "mass", _F32, (B, H, mb)), *more)
+    return dev, n, H, P, B, mb, out
 
 
 def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sel, q_seq=None, q_pos=None, *,
                     scale: float | None = None, out=None, mass=None, dev_err=None, stream=None) -> torch.Tensor:
     """sparse_attn over the 8-bit cache: bf16 [n_q, H, 128].  mass [B, H, max_blocks] fp32 (one query per
     sequence, q_seq None): each selected block's attention weight is added to its total."""
-    _dev(q, "q", torch.bfloat16, 3)
-    n_q, H = q.shape[0], q.shape[1]
-    _shape(q, "q", (n_q, H, HEAD_DIM))
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens)
-    B, mb = block_table.shape
-    _dev(sel, "sel", torch.int32, 2)
-    _shape(sel, "sel", (n_q, N_SEL))
-    _opt_i32(q_seq, "q_seq", n_q)
-    _opt_i32(q_pos, "q_pos", n_q)
-    _check_mass(mass, B, H, mb)
+    n_q = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    dev, n_q, H, P, B, mb, out = _attn_args(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
+        ((_need(sel, "sel"), "sel", _I32, (n_q, N_SEL)), (q_seq, "q_seq", _I32, (n_q,)), (q_pos, "q_pos", _I32, (n_q,))))
     if mass is not None and q_seq is not None:
         raise ValueError("mass needs one query per sequence: q_seq must be None")
-    out = _out(out, q)
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sel, q_seq, q_pos, out, mass,
-                      _dev_err(dev_err))
-    sc = float(scale) if scale is not None else HEAD_DIM ** -0.5
-    _launch("sparse_attn_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), _ptr(seq_lens), _ptr(q_seq), _ptr(q_pos), _ptr(sel), n_q, B, H, mb, k_cache.shape[0],
-            sc, _ptr(out), _ptr(mass), _ptr(dev_err))
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_sparse_attn_kv8, "sparse_attn_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            _at(q_seq), _at(q_pos), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
+            out.data_ptr(), _at(mass), _at(dev_err))
     return out
+
+
+_SCALE = HEAD_DIM ** -0.5
+
+
+def _need(t, name: str):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
 
 
 def sparse_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, *, out=None,
                       sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_decode over the 8-bit cache.  Returns (out [B,H,128] bf16, sel [B,16] int32)."""
-    _dev(q, "q", torch.bfloat16, 3)
-    _dev(idx_q, "idx_q", torch.bfloat16, 2)
-    _dev(idx_k_cache, "idx_k_cache", torch.bfloat16, 3)
-    B, H = q.shape[0], q.shape[1]
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens, B)
-    mb = block_table.shape[1]
-    out = _out(out, q)
+    dev = _device_of(q, "q", _BF16, 3)
+    B, P = q.shape[0], _pool(k_cache)
     if sel is None:
-        sel = torch.empty((B, N_SEL), dtype=torch.int32, device=q.device)
-    _dev(sel, "sel", torch.int32, 2)
-    _check_decode_args(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_lens, out, sel)
-    _check_mass(mass, B, H, mb)
-    workspace = _workspace(workspace, workspace_bytes(B, H, mb), q.device)
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, out, sel,
-                      mass, workspace, _dev_err(dev_err))
-    _launch("sparse_decode_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(idx_q), _ptr(idx_k_cache), _ptr(block_table), _ptr(seq_lens), B, H, mb, k_cache.shape[0], _ptr(out),
-            _ptr(sel), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+        sel = torch.empty((B, N_SEL), dtype=_I32, device=q.device)
+    dev, B, H, P, _, mb, out = _attn_args(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, B, out, mass,
+        ((sel, "sel", _I32, (B, N_SEL)), (_need(idx_q, "idx_q"), "idx_q", _BF16, (B, IDX_DIM)),
+         (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM))))
+    workspace = _space(workspace, lambda: workspace_bytes(B, H, mb), dev)
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_sparse_decode_kv8, "sparse_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), B, H, mb, P, out.data_ptr(), sel.data_ptr(), _at(mass),
+            workspace.data_ptr(), workspace.numel(), _at(dev_err))
     return out, sel
 
 
@@ -764,21 +813,14 @@ def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     """dense_decode over the 8-bit cache: blocks [0, ref_blocks) plus the 4-block local window, or all of them
     when ref_blocks is None.  Returns out [B,H,128] bf16; mass [B, H, max_blocks] receives every attended block's
     weight."""
-    _dev(q, "q", torch.bfloat16, 3)
-    B, H = q.shape[0], q.shape[1]
-    _shape(q, "q", (B, H, HEAD_DIM))
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens, B)
-    mb = block_table.shape[1]
-    rb = mb if ref_blocks is None else int(ref_blocks)
-    _check_mass(mass, B, H, mb)
-    out = _out(out, q)
-    workspace = _workspace(workspace, dense_kv8_workspace_bytes(B, H, mb), q.device)
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, mass, workspace,
-                      _dev_err(dev_err))
-    _launch("dense_decode_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), _ptr(seq_lens), rb, B, H, mb, k_cache.shape[0], _ptr(out), _ptr(mass), _ptr(workspace),
-            workspace.numel(), _ptr(dev_err))
+    n_seq = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_seq, out, mass)
+    workspace = _space(workspace, lambda: dense_kv8_workspace_bytes(B, H, mb), dev)
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_dense_decode_kv8, "dense_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            mb if ref_blocks is None else int(ref_blocks), B, H, mb, P, out.data_ptr(), _at(mass),
+            workspace.data_ptr(), workspace.numel(), _at(dev_err))
     return out
 
 
@@ -787,55 +829,37 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                         stream=None) -> torch.Tensor:
     """sparse_attn_seq over the 8-bit cache: many queries of sequence `seq` over the given selection.  Returns out
     [n_q,H,128] bf16; row `seq` of mass [B, H, max_blocks] receives the queries' weights."""
-    _dev(q, "q", torch.bfloat16, 3)
-    n_q, H = q.shape[0], q.shape[1]
-    _shape(q, "q", (n_q, H, HEAD_DIM))
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens)
-    B, mb = block_table.shape
-    _dev(q_pos, "q_pos", torch.int32, 1)
-    _shape(q_pos, "q_pos", (n_q,))
-    _dev(sel, "sel", torch.int32, 2)
-    _shape(sel, "sel", (n_q, N_SEL))
-    _check_mass(mass, B, H, mb)
-    out = _out(out, q)
-    workspace = _workspace(workspace, sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), q.device)
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, q_pos, sel, out, mass, workspace,
-                      _dev_err(dev_err))
-    sc = float(scale) if scale is not None else HEAD_DIM ** -0.5
-    _launch("sparse_attn_seq_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(block_table), _ptr(seq_lens), int(seq), _ptr(q_pos), _ptr(sel), n_q, B, H, mb, k_cache.shape[0], sc,
-            _ptr(out), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+    n_q = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
+    dev, n_q, H, P, B, mb, out = _attn_args(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
+        ((_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)), (_need(sel, "sel"), "sel", _I32, (n_q, N_SEL))))
+    workspace = _space(workspace, lambda: sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), dev)
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_sparse_attn_seq_kv8, "sparse_attn_seq_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+            int(seq), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
+            out.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
     return out
 
 
 def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, seq: int,
                        q_pos, *, out=None, sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_prefill over the 8-bit cache.  Returns (out [n_q,H,128] bf16, sel [n_q,16] int32)."""
-    _dev(q, "q", torch.bfloat16, 3)
-    _dev(idx_q, "idx_q", torch.bfloat16, 2)
-    _dev(idx_k_cache, "idx_k_cache", torch.bfloat16, 3)
-    _dev(q_pos, "q_pos", torch.int32, 1)
-    n_q, H = q.shape[0], q.shape[1]
-    _shape(q, "q", (n_q, H, HEAD_DIM))
-    _check_kv8(k_cache, v_cache, k_scale, v_scale, H)
-    _check_seqs(block_table, seq_lens)
-    B, mb = block_table.shape
-    _shape(idx_q, "idx_q", (n_q, IDX_DIM))
-    _shape(idx_k_cache, "idx_k_cache", (k_cache.shape[0], BLOCK, IDX_DIM))
-    _shape(q_pos, "q_pos", (n_q,))
+    dev = _device_of(q, "q", _BF16, 3)
+    n_q, P = q.shape[0], _pool(k_cache)
     if sel is None:
-        sel = torch.empty((n_q, N_SEL), dtype=torch.int32, device=q.device)
-    _dev(sel, "sel", torch.int32, 2)
-    _shape(sel, "sel", (n_q, N_SEL))
-    _check_mass(mass, B, H, mb)
-    out = _out(out, q)
-    workspace = _workspace(workspace, prefill_kv8_workspace_bytes(n_q, H, mb), q.device)
-    dev = _one_device(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, q_pos, out,
-                      sel, mass, workspace, _dev_err(dev_err))
-    _launch("sparse_prefill_kv8", dev, stream, _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-            _ptr(idx_q), _ptr(idx_k_cache), _ptr(block_table), _ptr(seq_lens), int(seq), _ptr(q_pos), n_q, B, H, mb,
-            k_cache.shape[0], _ptr(out), _ptr(sel), _ptr(mass), _ptr(workspace), workspace.numel(), _ptr(dev_err))
+        sel = torch.empty((n_q, N_SEL), dtype=_I32, device=q.device)
+    dev, n_q, H, P, B, mb, out = _attn_args(
+        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
+        ((sel, "sel", _I32, (n_q, N_SEL)), (_need(idx_q, "idx_q"), "idx_q", _BF16, (n_q, IDX_DIM)),
+         (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)),
+         (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,))))
+    workspace = _space(workspace, lambda: prefill_kv8_workspace_bytes(n_q, H, mb), dev)
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_sparse_prefill_kv8, "sparse_prefill_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
+            v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
+            block_table.data_ptr(), seq_lens.data_ptr(), int(seq), q_pos.data_ptr(), n_q, B, H, mb, P, out.data_ptr(),
+            sel.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
     return out, sel
 
 
@@ -845,26 +869,29 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
     and those of the others with the highest totals over the heads (lower id on ties) stay.  Returns (new_mass
     [B,H,max_blocks] fp32, new_table [B,max_blocks] int32, new_lens [B] int32, freed [B,max_blocks] int32 pages,
     n_freed [B] int32); the first three may be the inputs themselves."""
-    _dev(mass, "mass", torch.float32, 3)
-    _check_seqs(block_table, seq_lens)
-    B, mb = block_table.shape
-    H = mass.shape[1]
-    _check_mass(mass, B, H, mb)
+    dev = _device_of(mass, "mass", _F32, 3)
+    B, H, mb = mass.shape
     new_mass = torch.empty_like(mass) if new_mass is None else new_mass
     new_table = torch.empty_like(block_table) if new_table is None else new_table
     new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
     freed = torch.empty_like(block_table) if freed is None else freed
     n_freed = torch.empty_like(seq_lens) if n_freed is None else n_freed
-    _dev(new_mass, "new_mass", torch.float32, 3)
-    _shape(new_mass, "new_mass", (B, H, mb))
-    for t, n, shape in ((new_table, "new_table", (B, mb)), (new_lens, "new_lens", (B,)), (freed, "freed", (B, mb)),
-                        (n_freed, "n_freed", (B,))):
-        _dev(t, n, torch.int32, len(shape))
-        _shape(t, n, shape)
-    workspace = _workspace(workspace, evict_workspace_bytes(B, H, mb), mass.device)
-    dev = _one_device(mass, block_table, seq_lens, new_mass, new_table, new_lens, freed, n_freed, workspace,
-                      _dev_err(dev_err))
-    _launch("evict_blocks", dev, stream, _ptr(mass), _ptr(block_table), _ptr(seq_lens), B, H, mb, int(keep_blocks),
-            int(n_sink), _ptr(new_mass), _ptr(new_table), _ptr(new_lens), _ptr(freed), _ptr(n_freed), _ptr(workspace),
-            workspace.numel(), _ptr(dev_err))
+    table, lens = (B, mb), (B,)
+    try:
+        good = (_fits(block_table, _I32, table, dev) and _fits(seq_lens, _I32, lens, dev)
+                and _fits(new_mass, _F32, mass.shape, dev) and _fits(new_table, _I32, table, dev)
+                and _fits(new_lens, _I32, lens, dev) and _fits(freed, _I32, table, dev)
+                and _fits(n_freed, _I32, lens, dev))
+    except AttributeError:
+        good = False
+    if not good:
+        _refuse(dev, (block_table, "block_table", _I32, table), (seq_lens, "seq_lens", _I32, lens),
+                (new_mass, "new_mass", _F32, (B, H, mb)), (new_table, "new_table", _I32, table),
+                (new_lens, "new_lens", _I32, lens), (freed, "freed", _I32, table), (n_freed, "n_freed", _I32, lens))
+    workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev)
+    _check_dev_err(dev_err, dev)
+    _launch(_lib().uocr_evict_blocks, "evict_blocks", dev, stream, mass.data_ptr(), block_table.data_ptr(),
+            seq_lens.data_ptr(), B, H, mb, int(keep_blocks), int(n_sink), new_mass.data_ptr(), new_table.data_ptr(),
+            new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            _at(dev_err))
     return new_mass, new_table, new_lens, freed, n_freed

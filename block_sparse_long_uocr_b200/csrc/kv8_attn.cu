@@ -16,7 +16,8 @@ namespace uocr {
 
 namespace {
 
-// A warp's softmax state over one or more blocks: acc of lane (g, 0) holds dims 16 g .. 16 g + 15.
+// A warp's softmax state over one or more blocks: the sum of acc over the lanes c = 0, 1 of quad g
+// holds dims 16 g .. 16 g + 15.
 struct State8 {
     float m = -INFINITY, l = 0.f;
     float acc[16];
@@ -26,150 +27,232 @@ struct State8 {
     }
 };
 
-// One block: scores, softmax weights against the running maximum, weighted values.  Returns the
-// block's weight sum in units of 2^m (the state's new maximum).  `visible` >= 1 tokens count.
-__device__ __forceinline__ float attend8(State8 &st, const uint4 (&k)[8], uint4 (&v)[8], const Query8 &q, float ks,
-                                         float vs, float scale_log2, int visible, int lane) {
-    float z[4];
-    scores8(z, k, q, lane);
-    const float f = ks * scale_log2;
-    const int g = lane >> 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = z[i] * q.unit * f;
-    if (visible < kBlock) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (8 * i + g >= visible) z[i] = -INFINITY;
-        mask_v8(v, visible, lane);
-    }
-    float mb = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
-    const float m = fmaxf(st.m, mb);
-    const float base = m == -INFINITY ? 0.f : m;      // every score -inf: weights 0, not NaN
-    const float corr = exp2f(st.m - base);            // 0 on the first block
-    float p[4], lb = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        p[i] = exp2f(z[i] - base);
-        lb += p[i];
-    }
-#pragma unroll
-    for (int x = 4; x < 32; x <<= 1) lb += __shfl_xor_sync(0xffffffffu, lb, x);
-    st.m = m;
-    st.l = fmaf(st.l, corr, lb);
-#pragma unroll
-    for (int e = 0; e < 16; ++e) st.acc[e] *= corr;
-    weighted_sum8(st.acc, p, v, vs, lane);
-    return lb;
+// The blocks that a warp attends: lane t holds the t-th block's id, its page (-1: none) and scales.
+struct Blocks8 {
+    int j, page;
+    float ks, vs;
+};
+
+// The scales of the lane's block; by a whole warp, after j and page are set.
+__device__ __forceinline__ void load_scales8(Blocks8 &bl, const float *__restrict__ k_scale,
+                                             const float *__restrict__ v_scale, int H, int h) {
+    const size_t tile = (size_t)max(bl.page, 0) * H + h;
+    bl.ks = bl.page >= 0 ? __ldg(k_scale + tile) : 0.f;
+    bl.vs = bl.page >= 0 ? __ldg(v_scale + tile) : 0.f;
 }
 
-// Warp states merged over a CTA's warps.  s_acc [warps][128], s_ml [warps] {m, l}.
+// Attention over the warp's blocks with a running maximum; done(t, m, l): the t-th block's weight
+// sum l in units of 2^m.  A block's K and V are loaded together and used at once; what overlaps the
+// arithmetic are the other warps' loads (16 to 20 a SM).  Loading the next block's K into the
+// registers that the scores free was slower (266 against 215 us for 16 x 32768 tokens): it keeps 32
+// more registers alive through the weighted sum, which then spills.
+template <class Done>
+__device__ __forceinline__ void attend8(State8 &st, const Blocks8 &bl, const uint4 *__restrict__ kc,
+                                        const uint4 *__restrict__ vc, int H, int h, int p, float scale_log2,
+                                        const Query8 &q, int lane, Done done) {
+    const int g = lane >> 2;
+    for (unsigned left = __ballot_sync(0xffffffffu, bl.page >= 0); left; left &= left - 1) {
+        const int t = __ffs(left) - 1;
+        const size_t at = ((size_t)__shfl_sync(0xffffffffu, bl.page, t) * H + h) * kTile8U4;
+        uint4 k[8], v[8];
+        load_k8(k, kc + at, lane);
+        load_v8(v, vc + at, lane);
+        float z[4];
+        scores8(z, k, q, lane);
+        const float f = __shfl_sync(0xffffffffu, bl.ks, t) * scale_log2;
+        const int visible = p - __shfl_sync(0xffffffffu, bl.j, t) * kBlock + 1;   // at least 1
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = z[i] * q.unit * f;
+        if (visible < kBlock) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (8 * i + g >= visible) z[i] = -INFINITY;
+            mask_v8(v, visible, lane);
+        }
+        float mb = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+        const float m = fmaxf(st.m, mb);
+        const float base = m == -INFINITY ? 0.f : m;      // every score -inf: weights 0, not NaN
+        const float corr = exp2f(st.m - base);            // 0 on the first block
+        float w[4], lb = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = exp2f(z[i] - base);
+            lb += w[i];
+        }
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) lb += __shfl_xor_sync(0xffffffffu, lb, x);
+        st.m = m;
+        st.l = fmaf(st.l, corr, lb);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) st.acc[e] *= corr;
+        weighted_sum8(st.acc, w, v, __shfl_sync(0xffffffffu, bl.vs, t), lane);
+        done(t, m, lb);
+    }
+}
+
+// Warp states, to be merged over a CTA's warps.
 template <int kWarps>
 struct Merge8 {
     float acc[kWarps][kD];
-    float2 ml[kWarps];
+    float2 ml[kWarps];   // {m, l}
 };
 template <int kWarps>
 __device__ __forceinline__ void put_state8(Merge8<kWarps> &s, const State8 &st, int warp, int lane) {
     if (lane == 0) s.ml[warp] = make_float2(st.m, st.l);
+    float a[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) a[e] = st.acc[e] + __shfl_xor_sync(0xffffffffu, st.acc[e], 1);
     if ((lane & 3) == 0) {
         float4 *dst = reinterpret_cast<float4 *>(&s.acc[warp][16 * (lane >> 2)]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            dst[e] = make_float4(st.acc[4 * e], st.acc[4 * e + 1], st.acc[4 * e + 2], st.acc[4 * e + 3]);
+        for (int e = 0; e < 4; ++e) dst[e] = make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
+    }
+}
+// The merged state, by threads d < 128 after a barrier: thread d gets dim d of the output.
+template <int kWarps>
+__device__ __forceinline__ void merge8(const Merge8<kWarps> &s, int d, float &M, float &L, float &A) {
+    float2 ml[kWarps];
+    float a[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        ml[w] = s.ml[w];
+        a[w] = s.acc[w][d];
+    }
+    M = ml[0].x;
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, ml[w].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    L = A = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2f(ml[w].x - base);   // 0 for an empty state
+        L = fmaf(ml[w].y, f, L);
+        A = fmaf(a[w], f, A);
     }
 }
 
-__device__ __forceinline__ int checked_page(const int32_t *bt_row, int j, int num_pages, int lane, int32_t *dev_err) {
+// The page of block j; -1 and a flag when it is outside the pool.
+__device__ __forceinline__ int checked_page(const int32_t *bt_row, int j, int num_pages, int32_t *dev_err) {
     const int page = __ldg(bt_row + j);
     if ((unsigned)page < (unsigned)num_pages) return page;
-    if (lane == 0) flag_error(dev_err, UOCR_DEVERR_PAGE);
+    flag_error(dev_err, UOCR_DEVERR_PAGE);
     return -1;
 }
 
-constexpr int kSWarps = kSel;   // sparse: a warp per selected block
-constexpr int kDWarps = 4;      // dense: warps of a CTA, each every fourth block of its chunk
-constexpr int kDChunk = 16;     // dense: blocks of a chunk
+constexpr int kSWarps = 4;       // sparse: warps of a CTA
+constexpr int kDWarps = 4;       // dense: warps of a CTA, each every fourth block of its chunk
+constexpr int kMaxChunk = 16;    // dense: most blocks of a chunk
+constexpr size_t kFewChunks = 1480;   // dense: shorter chunks where there would be fewer CTAs than this
+constexpr int kMergeThreads = 512;
 
 }  // namespace
 
-// A CTA per (query, head), a warp per selection slot.
-__global__ void __launch_bounds__(kSWarps * 32)
-sparse_attn_kv8_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
+// A cluster of kCluster CTAs of 4 warps per (query, head); warp w of CTA r attends the selection slots
+// 4 r + w, + 4 kCluster, ...  With four CTAs every warp has one block, and the four meet in CTA 0
+// through its shared memory: an SM takes in 64 bytes a clock, so the 128 KiB of a (query, head)
+// alone keep one for 1 us (one CTA of 16 warps took 7.0 us for 10 pairs, four CTAs 5.0).  With
+// enough pairs to fill the SMs one CTA does all 16.
+template <int kCluster>
+__global__ void __launch_bounds__(kSWarps * 32, 5)
+sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
                        const float *__restrict__ k_scale, const float *__restrict__ v_scale,
                        const int32_t *__restrict__ bt, const int32_t *__restrict__ seq_lens,
                        const int32_t *__restrict__ q_seq, const int32_t *__restrict__ q_pos,
                        const int32_t *__restrict__ sel, int B, int H, int max_blocks, int num_pages,
                        float scale_log2, int implicit_local, __nv_bfloat16 *__restrict__ out,
                        float *__restrict__ mass, int32_t *dev_err) {
+    constexpr int kStep = kSWarps * kCluster, kPer = kSel / kStep;
     __shared__ __align__(16) Merge8<kSWarps> s;
-    __shared__ int s_j[kSWarps];
-    const int ih = blockIdx.x, i = ih / H, h = ih - i * H;
+    __shared__ __align__(16) Merge8<kCluster> s_all;   // of CTA 0: the CTAs' states
+    __shared__ Query8Smem s_q[kSWarps];
+    __shared__ float s_slot[4][kSel];                  // of CTA 0, per slot: m, l, block (as bits), total before
+    const int rank = kCluster > 1 ? cluster_rank() : 0;
+    if (kCluster > 1) cluster_arrive();
+    const int ih = blockIdx.x / kCluster, i = ih / H, h = ih - i * H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot = rank * kSWarps + warp + kStep * (lane % kPer);   // of the lanes below kPer
 
+    // the selection, the query and the lengths are on their way before any of them is used
+    const int32_t *my_sel = sel + (size_t)i * kSel + slot;
+    int j = implicit_local ? -2 : ld_pinned(my_sel);
+    const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
-    const bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err, threadIdx.x == 0 && h == 0, r);
-    int j = -2;
-    if (ok && implicit_local) {   // slots that do not depend on the scores (see sparse_attn.cu)
+    const bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err,
+                                  threadIdx.x == 0 && h == 0 && rank == 0, r);
+    if (!ok) j = -1;
+    if (j == -2) {   // after the selection kernel: slots that do not depend on the scores (see sparse_attn.cu)
         if (r.nb <= kSel)
-            j = warp < r.nb ? warp : -1;
-        else if (warp >= kRemote)
-            j = r.nb - kSel + warp;
+            j = slot < r.nb ? slot : -1;
+        else if (slot >= kRemote)
+            j = r.nb - kSel + slot;
     }
-    if (j == -2) {
+    if (__any_sync(0xffffffffu, j == -2)) {
         pdl_wait();
-        j = ok ? __ldg(sel + (size_t)i * kSel + warp) : -1;
+        if (j == -2) j = __ldcg(my_sel);
     }
+    if (lane >= kPer) j = -1;
     if (j >= 0 && j >= r.nb) {
-        if (lane == 0) flag_error(dev_err, UOCR_DEVERR_SEL);
+        flag_error(dev_err, UOCR_DEVERR_SEL);
         j = -1;
     }
-    const int page = j >= 0 ? checked_page(bt + (size_t)r.b * max_blocks, j, num_pages, lane, dev_err) : -1;
+    Blocks8 bl;
+    bl.page = j >= 0 ? checked_page(bt + (size_t)r.b * max_blocks, j, num_pages, dev_err) : -1;
+    const Query8 query = split_query8(s_q[warp], raw, lane);   // while the page is on its way
+    bl.j = bl.page >= 0 ? j : -1;
+    load_scales8(bl, k_scale, v_scale, H, h);
+    float *const totals = mass ? mass + ((size_t)(ok ? r.b : 0) * H + h) * max_blocks : nullptr;
+    const float before = totals && bl.j >= 0 ? __ldcg(totals + bl.j) : 0.f;   // in flight beside the attention
 
     State8 st;
-    if (page >= 0) {
-        const size_t tile = (size_t)page * H + h;
-        uint4 k[8], v[8];
-        load_k8(k, kc + tile * kTile8U4, lane);
-        load_v8(v, vc + tile * kTile8U4, lane);
-        const float ks = __ldg(k_scale + tile), vs = __ldg(v_scale + tile);
-        const Query8 qf = load_query8(q + (size_t)ih * (kD / 8), lane);
-        attend8(st, k, v, qf, ks, vs, scale_log2, min(kBlock, r.p - j * kBlock + 1), lane);
-    }
+    float2 mine = make_float2(-INFINITY, 0.f);   // of the lane's slot
+    attend8(st, bl, kc, vc, H, h, ok ? r.p : -1, scale_log2, query, lane, [&](int t, float m, float l) {
+        if (lane == t) mine = make_float2(m, l);
+    });
     put_state8(s, st, warp, lane);
-    if (lane == 0) s_j[warp] = page >= 0 ? j : -1;
+    if (kCluster > 1) cluster_wait();   // every CTA of the cluster has started
+    if (lane < kPer) {
+        const float put[4] = {mine.x, mine.y, __int_as_float(bl.j), before};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (kCluster > 1)
+                st_cluster(in_cta(&s_slot[x][slot], 0), put[x]);
+            else
+                s_slot[x][slot] = put[x];
+        }
+    }
     __syncthreads();
 
-    if (threadIdx.x < kD) {
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kSWarps; ++w) M = fmaxf(M, s.ml[w].x);
-        const float base = M == -INFINITY ? 0.f : M;
-        float L = 0.f, A = 0.f;
-#pragma unroll
-        for (int w = 0; w < kSWarps; ++w) {
-            const float f = exp2f(s.ml[w].x - base);   // 0 for an empty slot
-            L = fmaf(s.ml[w].y, f, L);
-            A = fmaf(s.acc[w][threadIdx.x], f, A);
-        }
+    const int d = threadIdx.x;   // one of 128
+    float M, L, A;
+    merge8(s, d, M, L, A);
+    if (kCluster > 1) {
+        st_cluster(in_cta(&s_all.acc[rank][d], 0), A);
+        if (d < 2) st_cluster(in_cta(reinterpret_cast<float *>(&s_all.ml[rank]) + d, 0), d ? L : M);
+        cluster_arrive();
+        cluster_wait();
+        if (rank == 0) merge8(s_all, d, M, L, A);
+    }
+    if (rank == 0) {
         // L is 0 for a query without a visible token, NaN where a score is
-        out[(size_t)ih * kD + threadIdx.x] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
-        if (mass && threadIdx.x < kSWarps && s_j[threadIdx.x] >= 0) {
+        out[(size_t)ih * kD + d] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
+        if (totals && warp == 0) {
             // one writer per block: the first slot that names it adds the weights of all that do
-            const int mine = s_j[threadIdx.x];
-            bool first = true;
-            float w = 0.f;
-#pragma unroll
-            for (int x = 0; x < kSWarps; ++x) {
-                if (s_j[x] != mine) continue;
-                if (x < (int)threadIdx.x) first = false;
-                w += s.ml[x].y * exp2f(s.ml[x].x - base);
+            const int x = lane & 15;
+            const int block = __float_as_int(s_slot[2][x]);
+            float w = s_slot[1][x] * exp2f(s_slot[0][x] - (M == -INFINITY ? 0.f : M));
+            const unsigned same = __match_any_sync(0xffffffffu, block) & 0xffffu;
+            if (__any_sync(0xffffffffu, block >= 0 && (same & (same - 1)))) {
+                float all = 0.f;
+                for (int y = 0; y < kSel; ++y) {
+                    const float o = __shfl_sync(0xffffffffu, w, y);
+                    if (same >> y & 1) all += o;
+                }
+                w = all;
             }
-            if (first && L > 0.f) {
-                float *m = mass + ((size_t)r.b * H + h) * max_blocks + mine;
-                *m += finite_weight(w / L);
-            }
+            if (lane < kSel && block >= 0 && lane == __ffs(same) - 1 && L > 0.f)
+                totals[block] = s_slot[3][x] + finite_weight(w / L);
         }
     }
     // warps whose blocks were known in advance did not wait for the selection kernel: this grid
@@ -177,108 +260,118 @@ sparse_attn_kv8_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ kc
     if (blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();
 }
 
-// Split over chunks of 16 blocks: CTA (query, head, chunk) leaves {m, l}, acc[128] and, for the
+// Split over chunks of blocks: CTA (query, head, chunk) leaves {m, l}, acc[128] and, for the
 // totals, each block's weight sum with the maximum it refers to.
-__global__ void __launch_bounds__(kDWarps * 32)
-dense_kv8_chunk_kernel(const uint4 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
+__global__ void __launch_bounds__(kDWarps * 32, 5)
+dense_kv8_chunk_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
                        const float *__restrict__ k_scale, const float *__restrict__ v_scale,
                        const int32_t *__restrict__ bt, const int32_t *__restrict__ seq_lens, int B, int H,
-                       int max_blocks, int num_pages, int ref_blocks, int n_chunks, float scale_log2,
-                       float *__restrict__ part_acc, float2 *__restrict__ part_ml, float2 *__restrict__ blk_ml,
-                       int32_t *dev_err) {
+                       int max_blocks, int num_pages, int ref_blocks, int chunk_blocks, int n_chunks,
+                       float scale_log2, float *__restrict__ part_acc, float2 *__restrict__ part_ml,
+                       float2 *__restrict__ blk_ml, int32_t *dev_err) {
     __shared__ __align__(16) Merge8<kDWarps> s;
+    __shared__ Query8Smem s_q[kDWarps];
     const int chunk = blockIdx.x % n_chunks, ih = blockIdx.x / n_chunks;
     const int i = ih / H, h = ih - i * H;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
     const bool ok = resolve_query(i, seq_lens, nullptr, nullptr, B, max_blocks, dev_err,
                                   threadIdx.x == 0 && chunk == 0 && h == 0, r);
     const int nb = ok ? r.nb : 0;
-    if (chunk * kDChunk >= nb) return;   // the merge reads only the chunks below nb
+    if (chunk * chunk_blocks >= nb) return;   // the merge reads only the chunks below nb
 
-    const Query8 qf = load_query8(q + (size_t)ih * (kD / 8), lane);
-    const int32_t *bt_row = bt + (size_t)r.b * max_blocks;
+    const int j = chunk * chunk_blocks + warp + kDWarps * lane;   // of the lanes below chunk_blocks / 4
+    const bool mine = lane < chunk_blocks / kDWarps && j < nb;
+    Blocks8 bl;
+    bl.j = j;
+    bl.page = mine && (j < ref_blocks || j >= nb - kLocal)
+                  ? checked_page(bt + (size_t)r.b * max_blocks, j, num_pages, dev_err)
+                  : -1;
+    const Query8 query = split_query8(s_q[warp], raw, lane);   // while the pages are on their way
+    load_scales8(bl, k_scale, v_scale, H, h);
+    if (blk_ml && mine && bl.page < 0) blk_ml[(size_t)ih * max_blocks + j] = make_float2(-INFINITY, 0.f);
     State8 st;
-    for (int x = warp; x < kDChunk; x += kDWarps) {
-        const int j = chunk * kDChunk + x;
-        if (j >= nb) break;
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (j < ref_blocks || j >= nb - kLocal) {
-            const int page = checked_page(bt_row, j, num_pages, lane, dev_err);
-            if (page >= 0) {
-                const size_t tile = (size_t)page * H + h;
-                uint4 k[8], v[8];
-                load_k8(k, kc + tile * kTile8U4, lane);
-                load_v8(v, vc + tile * kTile8U4, lane);
-                const float ks = __ldg(k_scale + tile), vs = __ldg(v_scale + tile);
-                ml.y = attend8(st, k, v, qf, ks, vs, scale_log2, min(kBlock, r.p - j * kBlock + 1), lane);
-                ml.x = st.m;
-            }
-        }
-        if (blk_ml && lane == 0) blk_ml[(size_t)ih * max_blocks + j] = ml;
-    }
+    attend8(st, bl, kc, vc, H, h, ok ? r.p : -1, scale_log2, query, lane,
+            [&](int t, float m, float l) {
+                if (blk_ml && lane == t) blk_ml[(size_t)ih * max_blocks + j] = make_float2(m, l);
+            });
     put_state8(s, st, warp, lane);
     __syncthreads();
     const int d = threadIdx.x;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kDWarps; ++w) M = fmaxf(M, s.ml[w].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f, A = 0.f;
-#pragma unroll
-    for (int w = 0; w < kDWarps; ++w) {
-        const float f = exp2f(s.ml[w].x - base);
-        L = fmaf(s.ml[w].y, f, L);
-        A = fmaf(s.acc[w][d], f, A);
-    }
-    const size_t slot = (size_t)ih * n_chunks + chunk;
-    part_acc[slot * kD + d] = A;
-    if (d == 0) part_ml[slot] = make_float2(M, L);
+    float M, L, A;
+    merge8(s, d, M, L, A);
+    const size_t at = (size_t)ih * n_chunks + chunk;
+    part_acc[at * kD + d] = A;
+    if (d == 0) part_ml[at] = make_float2(M, L);
 }
 
-// CTA (query, head, 0) merges the chunks' states into the output; CTA (query, head, 1 + x) adds the
-// weights of the blocks [128 x, 128 x + 128) to their totals.
-__global__ void __launch_bounds__(kD)
-dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int max_blocks, int n_chunks, int parts,
-                       const float *__restrict__ part_acc, const float2 *__restrict__ part_ml,
+// CTA (query, head, 0) merges the chunks' states into the output, a warp per every sixteenth chunk
+// and four dims per lane; CTA (query, head, 1 + x) adds the weights of the blocks [512 x, 512 x + 512)
+// to their totals.
+__global__ void __launch_bounds__(kMergeThreads)
+dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int max_blocks, int chunk_blocks, int n_chunks,
+                       int parts, const float4 *__restrict__ part_acc, const float2 *__restrict__ part_ml,
                        const float2 *__restrict__ blk_ml, __nv_bfloat16 *__restrict__ out, float *__restrict__ mass) {
-    __shared__ float s_red[kD / 32];
+    constexpr int kWarps = kMergeThreads / 32;
+    __shared__ float s_red[kWarps];
+    __shared__ float4 s_acc[kWarps][kD / 4];
     const int ih = blockIdx.x / parts, part = blockIdx.x - ih * parts;
-    const int i = ih / H, d = threadIdx.x;
+    const int i = ih / H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     QueryRef r;
     const bool ok = resolve_query(i, seq_lens, nullptr, nullptr, B, max_blocks, nullptr, false, r);
     const int nb = ok ? r.nb : 0;
-    const int used = (nb + kDChunk - 1) / kDChunk;
+    const int used = (nb + chunk_blocks - 1) / chunk_blocks;
+    if (part > 0 && (part - 1) * kMergeThreads >= nb) return;
+    const int j = (part - 1) * kMergeThreads + tid;
+    const bool add = part > 0 && j < nb;
+    const size_t at = (size_t)ih * max_blocks + j;
+    const float before = add ? mass[at] : 0.f;   // not written by the kernel before this one
     pdl_wait();
-    if (part > 0 && (part - 1) * kD >= nb) return;
+    const float2 own = add ? __ldcg(blk_ml + at) : make_float2(-INFINITY, 0.f);
     const float2 *ml = part_ml + (size_t)ih * n_chunks;
-    float M = -INFINITY;
-    for (int c = d; c < used; c += kD) M = fmaxf(M, ml[c].x);
-    M = warp_max(M);
-    if ((d & 31) == 0) s_red[d >> 5] = M;
+    // maximum and sum over the chunks, in an order that does not depend on the part
+    float2 st = make_float2(-INFINITY, 0.f);
+    for (int c = tid; c < used; c += kMergeThreads) {
+        const float2 x = __ldcg(ml + c);
+        const float m = fmaxf(st.x, x.x), b = m == -INFINITY ? 0.f : m;
+        st = make_float2(m, st.y * exp2f(st.x - b) + x.y * exp2f(x.x - b));
+    }
+    float M = warp_max(st.x);
+    if (lane == 0) s_red[warp] = M;
     __syncthreads();
-    M = fmaxf(fmaxf(s_red[0], s_red[1]), fmaxf(s_red[2], s_red[3]));
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_red[w]);
     __syncthreads();
     const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    for (int c = d; c < used; c += kD) L += ml[c].y * exp2f(ml[c].x - base);
-    L = warp_sum(L);
-    if ((d & 31) == 0) s_red[d >> 5] = L;
+    float L = warp_sum(st.y * exp2f(st.x - base));
+    if (lane == 0) s_red[warp] = L;
     __syncthreads();
-    L = s_red[0] + s_red[1] + s_red[2] + s_red[3];
-    if (part == 0) {
+    L = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) L += s_red[w];
+    if (part > 0) {
+        if (add && L > 0.f) mass[at] = before + finite_weight(own.y * exp2f(own.x - base) / L);
+        return;
+    }
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int c = warp; c < used; c += kWarps) {
+        const float f = exp2f(__ldcg(ml + c).x - base);
+        const float4 v = __ldcg(part_acc + ((size_t)ih * n_chunks + c) * (kD / 4) + lane);
+        a.x = fmaf(v.x, f, a.x);
+        a.y = fmaf(v.y, f, a.y);
+        a.z = fmaf(v.z, f, a.z);
+        a.w = fmaf(v.w, f, a.w);
+    }
+    s_acc[warp][lane] = a;
+    __syncthreads();
+    if (tid < kD) {
         float A = 0.f;
-#pragma unroll 8
-        for (int c = 0; c < used; ++c)
-            A = fmaf(part_acc[((size_t)ih * n_chunks + c) * kD + d], exp2f(ml[c].x - base), A);
-        out[(size_t)ih * kD + d] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
-    } else if (L > 0.f) {
-        const int j = (part - 1) * kD + d;
-        if (j < nb) {
-            const float2 b = blk_ml[(size_t)ih * max_blocks + j];
-            mass[(size_t)ih * max_blocks + j] += finite_weight(b.y * exp2f(b.x - base) / L);
-        }
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) A += reinterpret_cast<const float *>(s_acc[w])[tid];
+        out[(size_t)ih * kD + tid] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
     }
 }
 
@@ -289,28 +382,44 @@ cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8C
                                    float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err) {
     const long long grid = (long long)n_q * H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    // As many CTAs per pair as can all be resident at once, 5 a SM.  Measured with 1 / 2 / 4 (us; 148
+    // SMs): 10 pairs 7.2 / 6.1 / 5.0, 140: 10.8 / 9.0 / 8.5, 200: 11.9 / 10.0 / 14.6, 300: 13.8 /
+    // 12.7 / 16.7, 450: 15.4 / 20.0 / 22.9.
+    const int cluster = 4 * grid <= 5 * c.num_sms ? 4 : 2 * grid <= 5 * c.num_sms ? 2 : 1;
+    attr[0].val.clusterDim.x = cluster;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
+    cfg.gridDim = dim3((unsigned)(cluster * grid));
     cfg.blockDim = dim3(kSWarps * 32);
     cfg.stream = c.stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = c.pdl ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, sparse_attn_kv8_kernel, (const uint4 *)q, (const uint4 *)kv.k, (const uint4 *)kv.v,
-                              kv.k_scale, kv.v_scale, bt, seq_lens, q_seq, q_pos, sel, B, H, max_blocks, num_pages,
-                              scale * kLog2e, implicit_local ? 1 : 0, (__nv_bfloat16 *)out, mass, dev_err);
+    cfg.attrs = cluster > 1 ? attr : attr + 1;
+    cfg.numAttrs = (cluster > 1 ? 1 : 0) + (c.pdl ? 1 : 0);
+    return cudaLaunchKernelEx(&cfg, cluster == 4   ? sparse_attn_kv8_kernel<4>
+                                    : cluster == 2 ? sparse_attn_kv8_kernel<2>
+                                                   : sparse_attn_kv8_kernel<1>, (const uint2 *)q,
+                              (const uint4 *)kv.k, (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, q_seq,
+                              q_pos, sel, B, H, max_blocks, num_pages, scale * kLog2e, implicit_local ? 1 : 0,
+                              (__nv_bfloat16 *)out, mass, dev_err);
 }
 
 namespace {
 struct Dense8Ws {
+    int chunk_blocks, n_chunks;
     size_t acc_off, ml_off, blk_off, total;
 };
 Dense8Ws dense8_layout(int n_q, int H, int max_blocks) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t rows = (size_t)n_q * H, slots = rows * ((max_blocks + kDChunk - 1) / kDChunk);
     Dense8Ws w{};
+    const size_t rows = (size_t)n_q * H;
+    w.chunk_blocks = kMaxChunk;
+    while (w.chunk_blocks > kDWarps && rows * ((max_blocks + w.chunk_blocks - 1) / w.chunk_blocks) < kFewChunks)
+        w.chunk_blocks /= 2;
+    w.n_chunks = (max_blocks + w.chunk_blocks - 1) / w.chunk_blocks;
+    const size_t slots = rows * w.n_chunks;
     w.ml_off = up(slots * kD * 4);
     w.blk_off = w.ml_off + up(slots * sizeof(float2));
     w.total = w.blk_off + up(rows * max_blocks * sizeof(float2));
@@ -324,12 +433,11 @@ cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &
                              const int32_t *seq_lens, int B, int H, int max_blocks, int num_pages, int ref_blocks,
                              float scale, void *out, float *mass, void *ws, int32_t *dev_err) {
     const Dense8Ws w = dense8_layout(B, H, max_blocks);
-    const int n_chunks = (max_blocks + kDChunk - 1) / kDChunk;
     float *acc = (float *)((char *)ws + w.acc_off);
     float2 *ml = (float2 *)((char *)ws + w.ml_off);
     float2 *blk = mass ? (float2 *)((char *)ws + w.blk_off) : nullptr;
-    const long long grid = (long long)B * H * n_chunks;
-    const int parts = mass ? 1 + (max_blocks + kD - 1) / kD : 1;
+    const long long grid = (long long)B * H * w.n_chunks;
+    const int parts = mass ? 1 + (max_blocks + kMergeThreads - 1) / kMergeThreads : 1;
     if (grid > 0x7fffffffLL || (long long)B * H * parts > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -338,16 +446,16 @@ cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kDWarps * 32);
     cfg.stream = c.stream;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, dense_kv8_chunk_kernel, (const uint4 *)q, (const uint4 *)kv.k,
+    cudaError_t e = cudaLaunchKernelEx(&cfg, dense_kv8_chunk_kernel, (const uint2 *)q, (const uint4 *)kv.k,
                                        (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, B, H, max_blocks,
-                                       num_pages, ref_blocks, n_chunks, scale * kLog2e, acc, ml, blk, dev_err);
+                                       num_pages, ref_blocks, w.chunk_blocks, w.n_chunks, scale * kLog2e, acc, ml, blk, dev_err);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(B * H * parts));
-    cfg.blockDim = dim3(kD);
+    cfg.blockDim = dim3(kMergeThreads);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dense_kv8_merge_kernel, seq_lens, B, H, max_blocks, n_chunks, parts,
-                              (const float *)acc, (const float2 *)ml, (const float2 *)blk, (__nv_bfloat16 *)out, mass);
+    return cudaLaunchKernelEx(&cfg, dense_kv8_merge_kernel, seq_lens, B, H, max_blocks, w.chunk_blocks,
+                              w.n_chunks, parts, (const float4 *)acc, (const float2 *)ml, (const float2 *)blk, (__nv_bfloat16 *)out, mass);
 }
 
 }  // namespace uocr

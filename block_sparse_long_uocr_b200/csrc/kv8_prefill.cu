@@ -76,7 +76,7 @@ kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel,
 #pragma unroll
         for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
         float inv;
-        const float s = f16_row_scale(amax, inv);
+        const float s = row_scale<14>(amax, inv);
         if (live) {
             // dims 8 l ..: half l / 8, c = (l % 8) / 2, x % 2 = l % 2
             const int piece = 4 * (2 * (l >> 3) + (l & 1)) + ((l & 7) >> 1);

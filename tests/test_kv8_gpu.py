@@ -452,6 +452,24 @@ def test_evict(uocr, cuda_device, mb, H, kind, in_place):
             assert torch.equal(w.view(torch.int32) if w.is_floating_point() else w, x.view(torch.int32) if x.is_floating_point() else x), (name, keep, sink)
 
 
+@pytest.mark.parametrize("H", [1, 3])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_evict_tables_beyond_shared_memory(uocr, cuda_device, H, in_place):
+    """Long tables take another launch plan; sequences that keep, cut a little and cut nearly everything."""
+    g = torch.Generator().manual_seed(50 + H)
+    B, mb = 3, 30001
+    mass = torch.exp(2 * torch.randn((B, H, mb), generator=g))
+    mass[:, :, ::3] = 0.0
+    table = torch.randint(0, 1 << 20, (B, mb), generator=g, dtype=torch.int32)
+    lens = torch.tensor([mb * BLOCK - 5, 9000 * BLOCK, 20000 * BLOCK + 1], dtype=torch.int32)
+    for keep, sink in ((9500, 3), (29000, 0), (4, 0)):
+        want = ref.evict(mass, table, lens, keep, sink)
+        got, err = run_evict(uocr, cuda_device, mass, table, lens, keep, sink, in_place)
+        assert err == 0
+        for w, x, name in zip(want, got, ("mass", "table", "lens", "freed", "n_freed")):
+            assert torch.equal(w, x), (name, keep, sink)
+
+
 def test_evict_bad_lengths_copy_and_flag(uocr, cuda_device):
     mass, table = torch.rand((3, 2, 50)), torch.arange(150, dtype=torch.int32).reshape(3, 50)
     lens = torch.tensor([-1, 50 * BLOCK + 1, 1000], dtype=torch.int32)
