@@ -13,14 +13,22 @@
 // exponents: they are rounded again only where they fall below e4m3's normal range.  It only
 // rises, and rows that are already cached keep their codes unless it does.
 //
-// x is the rotated key in 64 bits (angles, sines and products) rounded once, to nearest even: on
-// its way through 32 bits it is rounded to odd, which no later rounding to fewer bits can see.  So
+// x is the rotated key in 64 bits (angles, sines; products in 64 bits or as sums of two fp32
+// numbers) rounded once, to nearest even: on its way through 32 bits it is rounded to odd, which no
+// later rounding to fewer bits can see.  So
 // a code is a function of its inputs' exact values, the same whatever chunk its token came in.
 // Infinities and NaN are stored as e4m3's NaN (it has no infinity, and a saturated one would look
 // like a value).
 //
-// Layout: CTA (run, head), a run being the new tokens of one sequence that fall in one page; head
-// index H stands for the indexer's vectors, which stay bf16.
+// Layout: a run is the new tokens of one sequence that fall in one page; head index H stands for the
+// indexer's vectors, which stay bf16.  Two kernels:
+//   few tokens a sequence (decode): CTA (run, head), a thread per (token, pair); what counts is the
+//       latency of one sine and one reduction.  64 sequences of one token, 10 heads: 4.4 us.
+//   many: CTA (run, a few heads), thread (token, 8 pairs) of 32 tokens: the sines of a page are
+//       formed once for the CTA's heads and kept in registers, every load and store is 8 or 16 bytes.
+//       2048 tokens, 10 heads: 27.7 us with the first kernel (11 times the sines, 64-bit conversions
+//       at 16 a clock), 14.5 here: bound by the issue of the rotation's two-number products (about
+//       900 instructions a thread and head) and one barrier a head, not by its 28 MB (4.3 us).
 #include <math.h>
 
 #include "kernels.h"
@@ -121,7 +129,7 @@ __device__ __forceinline__ bool find_run(int r, const int32_t *__restrict__ star
 }  // namespace
 
 __global__ void __launch_bounds__(kAppThreads)
-rope_append_kv8_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, const __nv_bfloat16 *__restrict__ k_new,
+rope_append_kv8_few_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, const __nv_bfloat16 *__restrict__ k_new,
                        const __nv_bfloat16 *__restrict__ v_new, const __nv_bfloat16 *__restrict__ idx_k_new,
                        const int32_t *__restrict__ tok_pos, const int32_t *__restrict__ page_pos,
                        const int32_t *__restrict__ start, const int32_t *__restrict__ bt,
@@ -207,6 +215,215 @@ rope_append_kv8_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, const
     }
 }
 
+namespace {
+constexpr int kManyThreads = kBlock * kPairs / 8;   // thread (token, 8 pairs)
+
+// hi + lo, |lo| at most half a unit of hi, rounded to odd.
+__device__ __forceinline__ float round_odd(float hi, float lo) {
+    if (lo == 0.f) return hi;   // (keeps the sign of a zero)
+    const float s = __fadd_rz(hi, lo);
+    return (hi - s) + lo != 0.f && isfinite(s) ? __uint_as_float(__float_as_uint(s) | 1u) : s;
+}
+
+// a x + b y to about 2^-46 of its terms, rounded to odd; a and b as sums of two fp32 numbers.
+__device__ __forceinline__ float dot2_odd(float x, float ah, float al, float y, float bh, float bl) {
+    const float p = x * ah, pe = fmaf(x, ah, -p);
+    const float q = y * bh, qe = fmaf(y, bh, -q);
+    const float s = p + q, t = s - p;
+    const float e = (p - (s - t)) + (q - t);
+    return round_odd(s, fmaf(x, al, fmaf(y, bl, e + (pe + qe))));
+}
+
+// a x + b y to fp32, also where the terms cancel: the products' errors and the low parts added.
+__device__ __forceinline__ float dot2(float x, float ah, float al, float y, float bh, float bl) {
+    const float q = y * bh;
+    return fmaf(x, ah, q) + (fmaf(y, bh, -q) + fmaf(x, al, y * bl));
+}
+
+// Eight numbers (times inv) to packed codes; what is not finite to NaN.
+__device__ __forceinline__ uint2 pack_e4m3(const float *x, float inv) {
+    uint16_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float nan = __uint_as_float(0x7fffffffu);
+        const float a = isfinite(x[2 * k]) ? x[2 * k] * inv : nan, b = isfinite(x[2 * k + 1]) ? x[2 * k + 1] * inv : nan;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r[k]) : "f"(b), "f"(a));
+    }
+    return make_uint2((uint32_t)r[0] | (uint32_t)r[1] << 16, (uint32_t)r[2] | (uint32_t)r[3] << 16);
+}
+
+// 16 codes times ratio, to codes.
+__device__ __forceinline__ uint4 rescale_e4m3(uint4 v, float ratio) {
+    uint32_t out[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        uint32_t lo, hi;
+        e4m3x4_to_f16(word(v, w), lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        uint16_t r0, r1;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r0) : "f"(a.y * ratio), "f"(a.x * ratio));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r1) : "f"(b.y * ratio), "f"(b.x * ratio));
+        out[w] = (uint32_t)r0 | (uint32_t)r1 << 16;
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+__device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        r[k] = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+}  // namespace
+
+__global__ void __launch_bounds__(kManyThreads)
+rope_append_kv8_many_kernel(const uint4 *q, const uint4 *idx_q, const uint4 *__restrict__ k_new,
+                            const uint4 *__restrict__ v_new, const uint4 *__restrict__ idx_k_new,
+                            const int32_t *__restrict__ tok_pos, const int32_t *__restrict__ page_pos,
+                            const int32_t *__restrict__ start, const int32_t *__restrict__ bt,
+                            const int32_t *__restrict__ seq_lens, int n, int B, int H, int max_blocks,
+                            int num_pages, int group, uint4 *q_out, uint4 *idx_q_out, uint8_t *__restrict__ k_cache,
+                            uint8_t *__restrict__ v_cache, float *__restrict__ k_scale,
+                            float *__restrict__ v_scale, uint4 *__restrict__ idx_k_cache, RopeFreqs freqs,
+                            int32_t *dev_err) {
+    constexpr int kWarps = kManyThreads / 32;
+    __shared__ float2 s_red[2][kWarps];
+    const int tid = threadIdx.x, t = tid >> 3, c = tid & 7;   // token of the run, pairs 8 c .. 8 c + 7
+    const int h0 = blockIdx.y * group, h1 = min(H + 1, h0 + group);
+    Run run;
+    if (!find_run(blockIdx.x, start, seq_lens, n, B, max_blocks, dev_err, tid == 0 && h0 == 0, run)) return;
+    int page = __ldg(bt + (size_t)run.b * max_blocks + run.lp);
+    if ((unsigned)page >= (unsigned)num_pages) {
+        if (tid == 0 && h0 == 0) flag_error(dev_err, UOCR_DEVERR_PAGE);
+        page = -1;
+    }
+    const bool mine = t < run.count;
+    const int i = run.first + (mine ? t : 0);
+    // cosines and sines of the thread's pairs, as sums of two fp32 numbers
+    float ch[8], cl[8], sh[8], sl[8];
+    if (mine) {
+        const int page_mod2 = ((__ldg(page_pos + i) % 2) + 2) % 2;
+        const double tok = (double)__ldg(tok_pos + i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int pair = 8 * c + e;
+            double sn, cs;
+            sincos((pair < kPairs - UOCR_ROPE_PAGE_PAIRS ? tok : (double)page_mod2) * freqs.inv[pair], &sn, &cs);
+            ch[e] = (float)cs;
+            cl[e] = (float)(cs - (double)ch[e]);
+            sh[e] = (float)sn;
+            sl[e] = (float)(sn - (double)sh[e]);
+        }
+    }
+
+    for (int h = h0; h < h1; ++h) {
+        const bool idx = h == H;
+        const size_t row = (idx ? (size_t)i : (size_t)i * H + h) * (kD / 8);
+        uint4 qv[2], kv[2], vv[2];
+        float2 old = make_float2(0.f, 0.f);
+        const size_t tile = (size_t)max(page, 0) * H + (idx ? 0 : h);
+        if (mine) {
+            const uint4 *src = idx ? idx_q : q;
+            qv[0] = src[row + c];
+            qv[1] = src[row + 8 + c];
+            src = idx ? idx_k_new : k_new;
+            kv[0] = __ldg(src + row + c);
+            kv[1] = __ldg(src + row + 8 + c);
+            if (!idx) {
+                vv[0] = __ldg(v_new + row + 2 * c);
+                vv[1] = __ldg(v_new + row + 2 * c + 1);
+            }
+        }
+        // read before any thread of the CTA writes the new ones
+        if (!idx && run.row > 0 && page >= 0) old = make_float2(k_scale[tile], v_scale[tile]);
+
+        float y[16], v[16];   // half of the rotated key (dims 8 c .. and 64 + 8 c ..), half of the values
+        float2 top = make_float2(0.f, 0.f);
+        if (mine) {
+            float x0[8], x1[8], o0[8], o1[8];
+            bf16x8_to_f32(qv[0], x0);
+            bf16x8_to_f32(qv[1], x1);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                o0[e] = dot2(x0[e], ch[e], cl[e], -x1[e], sh[e], sl[e]);
+                o1[e] = dot2(x1[e], ch[e], cl[e], x0[e], sh[e], sl[e]);
+            }
+            uint4 *dst = idx ? idx_q_out : q_out;
+            dst[row + c] = pack_bf16x8(o0);
+            dst[row + 8 + c] = pack_bf16x8(o1);
+            bf16x8_to_f32(kv[0], x0);
+            bf16x8_to_f32(kv[1], x1);
+            if (idx) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    o0[e] = dot2(x0[e], ch[e], cl[e], -x1[e], sh[e], sl[e]);
+                    o1[e] = dot2(x1[e], ch[e], cl[e], x0[e], sh[e], sl[e]);
+                }
+                if (page >= 0) {
+                    uint4 *to = idx_k_cache + ((size_t)page * kBlock + run.row + t) * (kDIdx / 8);
+                    to[c] = pack_bf16x8(o0);
+                    to[8 + c] = pack_bf16x8(o1);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float a = 0.5f * x0[e], b = 0.5f * x1[e];
+                    y[e] = dot2_odd(a, ch[e], cl[e], -b, sh[e], sl[e]);
+                    y[8 + e] = dot2_odd(b, ch[e], cl[e], a, sh[e], sl[e]);
+                }
+                float w[8];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    bf16x8_to_f32(vv[k], w);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[8 * k + e] = 0.5f * w[e];
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    if (isfinite(y[e])) top.x = fmaxf(top.x, fabsf(y[e]));
+                    if (isfinite(v[e])) top.y = fmaxf(top.y, fabsf(v[e]));
+                }
+            }
+        }
+        if (idx || page < 0) continue;   // uniform over the CTA
+        top = make_float2(warp_max(top.x), warp_max(top.y));
+        float2(&red)[kWarps] = s_red[h & 1];   // two in turn: one barrier a head
+        if ((tid & 31) == 0) red[tid >> 5] = top;
+        __syncthreads();
+        float2 amax = red[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) amax = make_float2(fmaxf(amax.x, red[w].x), fmaxf(amax.y, red[w].y));
+        int ek = scale_exp(amax.x), ev = scale_exp(amax.y);
+        uint8_t *kt = k_cache + tile * kTile8, *vt = v_cache + tile * kTile8;
+        if (run.row > 0) {
+            ek = max(ek, scale_exp_of(old.x));
+            ev = max(ev, scale_exp_of(old.y));
+            const float rk = old.x / exp2i(ek), rv = old.y / exp2i(ev);
+            if (t < run.row) {   // older row t, 16 codes
+                uint4 *k16 = reinterpret_cast<uint4 *>(kt) + tid, *v16 = reinterpret_cast<uint4 *>(vt) + tid;
+                if (rk != 1.f) *k16 = rescale_e4m3(*k16, rk);
+                if (rv != 1.f) *v16 = rescale_e4m3(*v16, rv);
+            }
+        }
+        if (mine) {
+            const float ik = exp2i(1 - ek), iv = exp2i(1 - ev);
+            uint8_t *kr = kt + (run.row + t) * kD, *vr = vt + (run.row + t) * kD;
+            *reinterpret_cast<uint2 *>(kr + 8 * c) = pack_e4m3(y, ik);
+            *reinterpret_cast<uint2 *>(kr + 64 + 8 * c) = pack_e4m3(y + 8, ik);
+            const uint2 a = pack_e4m3(v, iv), b = pack_e4m3(v + 8, iv);
+            *reinterpret_cast<uint4 *>(vr + 16 * c) = make_uint4(a.x, a.y, b.x, b.y);
+        }
+        if (tid == 0) {
+            k_scale[tile] = exp2i(ek);
+            v_scale[tile] = exp2i(ev);
+        }
+    }
+}
+
 cudaError_t launch_rope_append_kv8(const LaunchCtx &c, const void *q, const void *idx_q, const void *k_new,
                                    const void *v_new, const void *idx_k_new, const int32_t *tok_pos,
                                    const int32_t *page_pos, const int32_t *start, const int32_t *bt,
@@ -215,7 +432,22 @@ cudaError_t launch_rope_append_kv8(const LaunchCtx &c, const void *q, const void
                                    float *v_scale, void *idx_k_cache, int32_t *dev_err) {
     const long long runs = start ? (long long)n / kBlock + 2ll * B : n;
     if (runs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    rope_append_kv8_kernel<<<dim3((unsigned)runs, (unsigned)(H + 1)), kAppThreads, 0, c.stream>>>(
+    // Measured with few / many (us, 10 heads; sequences x tokens): 1 x 4 4.8 / 5.0, 1 x 8 6.5 / 5.1,
+    // 1 x 2048 27.7 / 14.5, 16 x 4 6.1 / 6.2, 16 x 8 8.2 / 6.8, 64 x 1 4.6 / 9.8, 64 x 8 12.5 / 13.0,
+    // 64 x 16 19.8 / 13.7.
+    if ((long long)n > 6ll * B) {
+        // about two CTAs a SM: more would form the same sines more often
+        const int groups = (int)min((long long)H + 1, max(1ll, 2ll * c.num_sms / (n / kBlock + B)));
+        const int group = (H + 1 + groups - 1) / groups;
+        rope_append_kv8_many_kernel<<<dim3((unsigned)runs, (unsigned)((H + 1 + group - 1) / group)), kManyThreads, 0,
+                                      c.stream>>>(
+            (const uint4 *)q, (const uint4 *)idx_q, (const uint4 *)k_new, (const uint4 *)v_new, (const uint4 *)idx_k_new,
+            tok_pos, page_pos, start, bt, seq_lens, n, B, H, max_blocks, num_pages, group, (uint4 *)q_out,
+            (uint4 *)idx_q_out, (uint8_t *)k_cache, (uint8_t *)v_cache, k_scale, v_scale, (uint4 *)idx_k_cache,
+            rope_freqs(), dev_err);
+        return cudaGetLastError();
+    }
+    rope_append_kv8_few_kernel<<<dim3((unsigned)runs, (unsigned)(H + 1)), kAppThreads, 0, c.stream>>>(
         (const __nv_bfloat16 *)q, (const __nv_bfloat16 *)idx_q, (const __nv_bfloat16 *)k_new,
         (const __nv_bfloat16 *)v_new, (const __nv_bfloat16 *)idx_k_new, tok_pos, page_pos, start, bt, seq_lens, n, B, H,
         max_blocks, num_pages, (__nv_bfloat16 *)q_out, (__nv_bfloat16 *)idx_q_out, (uint8_t *)k_cache,

@@ -117,15 +117,18 @@ rope_append_kernel(__nv_bfloat16 *__restrict__ q, __nv_bfloat16 *__restrict__ id
 }
 
 RopeFreqs rope_freqs() {
-    RopeFreqs f;
-    const int n_tok = kPairs - UOCR_ROPE_PAGE_PAIRS;
-    for (int i = 0; i < kPairs; ++i) {
-        if (i < n_tok)
-            f.inv[i] = pow((double)UOCR_ROPE_THETA_TOKEN, -(double)i / (double)n_tok);
-        else
-            f.inv[i] = pow((double)UOCR_ROPE_THETA_PAGE, -(double)(i - n_tok) / (double)UOCR_ROPE_PAGE_PAIRS);
-    }
-    return f;
+    static const RopeFreqs freqs = [] {   // 64 powers, formed once a process
+        RopeFreqs f;
+        const int n_tok = kPairs - UOCR_ROPE_PAGE_PAIRS;
+        for (int i = 0; i < kPairs; ++i) {
+            if (i < n_tok)
+                f.inv[i] = pow((double)UOCR_ROPE_THETA_TOKEN, -(double)i / (double)n_tok);
+            else
+                f.inv[i] = pow((double)UOCR_ROPE_THETA_PAGE, -(double)(i - n_tok) / (double)UOCR_ROPE_PAGE_PAIRS);
+        }
+        return f;
+    }();
+    return freqs;
 }
 
 cudaError_t launch_rope_append(const LaunchCtx &c, void *q, void *idx_q, const void *k_new, const void *v_new,

@@ -138,7 +138,8 @@ def evict(mass, table, lens, keep, sink):
         cand = list(range(sink, nb - N_LOCAL))
         cand.sort(key=lambda j: (1, 0.0, j) if math.isnan(total[j]) else (0, -total[j], j))
         gone = sorted(cand[keep - sink - N_LOCAL:])
-        kept = [j for j in range(mb) if j not in set(gone)]
+        out = set(gone)
+        kept = [j for j in range(mb) if j not in out]
         m[b] = 0
         m[b, :, :len(kept)] = mass[b][:, kept]
         t[b] = -1
