@@ -1,33 +1,30 @@
 // kv8.cuh -- warp-level tile products over a key / value cache held in 8 bits (e4m3).
 //
 // Cache layout: codes [P][H][32][128] of one byte (a (page, head) tile is 4 KiB, contiguous) and
-// one fp32 scale per (page, head) for K and one for V: value = code * scale.  The codes go to the
-// tensor cores as they are (mma.sync m16n8k32, e4m3 in, fp32 accumulate); the other operand, a
-// query or the softmax weights, is written as a sum of a few e4m3 numbers times powers of 2^-5,
-//   x = c0 + 2^-5 c1 + 2^-10 c2,  c0 = e4m3(x), c1 = e4m3(2^5 (x - c0)), ...
-// each of which removes at least 5 bits of what is left (x is first scaled to below 2^8), and
-// each of which takes one of the 8 columns of B: a decode step has one query row per (sequence,
-// head), so the columns cost nothing.  Scales are applied to the fp32 results.
-//   - three terms hold a bf16 query to 2^-27 of its row's largest element (a number's 8 bits are
-//     exact after two, wherever it is not 2^-14 below the largest);
-//   - three terms hold a weight in [0, 1] to 2^-13 of itself;
-//   - the products' sums were checked against 64 bits: within 2^-22 of the sum of magnitudes over
-//     128 terms (random codes, chained accumulation), as fp32 FMAs would be.
-// Measured on a B200 (instructions a clock and SM): this MMA 0.94, m16n8k16 in fp16 0.50, a byte
-// permute 2.0, e4m3x2 -> f16x2 1.9; turning codes into fp16 first costs the tile 128 conversions a
-// lane and twice the MMAs at half their rate.
+// one fp32 scale per (page, head) for K and one for V: value = code * scale.  An e4m3 code is an
+// fp16 number exactly (4 significant bits, 2^-9 .. 448), so the tile products run on the fp16
+// tensor cores with fp32 accumulation and the scale is applied to their fp32 results: neither K
+// nor V is rounded again.  A query row is scaled by a power of two to fp16's range (exact, below);
+// a softmax weight is the sum of two fp16 numbers in two columns of B, which a single query leaves
+// free, so 22 bits of it are kept.
+//
+// The codes cannot go to the tensor cores as they are: mma.sync m16n8k32 on e4m3 operands runs on a
+// B200 as two fp16 MMAs and some 17 further instructions (counted: 19.9 issued per MMA with its
+// operand loads against 6.6 for the fp16 one), which converts every operand at every use.  Converted
+// once, a tile costs a lane 128 conversions (two codes each, 1.9 warp instructions a clock and SM)
+// and 32 MMAs (0.5 a clock).
 //
 // Fragments.  The contraction index of an MMA may be permuted as long as both operands agree, so
 // lane (g, c) = (lane / 4, lane % 4) takes its operand elements as whole 16-byte pieces of a row,
 // straight from global memory into registers (no staging, no shuffles, full 32-byte sectors):
 //   K, rows g + 8 i (i = 0..3): pieces c and c + 4 of the row (dims 16 c .. + 15 and 64 + 16 c .. + 15);
-//      a register holds 4 dims, two make one 32-dim MMA step of the row;
-//   V: piece g (dims 16 g .. 16 g + 15) of the 8 tokens 4 x + c; a 4 x 4 byte transpose (8 permutes)
-//      turns four tokens' words into the registers of four dims, four tokens each.
-// The scores of tokens g + 8 i come out in quad g, and one register of B holds four tokens of one
-// column: a quad's four weights, packed, are what lane c = g % 4 of a column needs.
-// These are the warp-level MMAs: a decode step has one query row per (sequence, head), and an item
-// of a prefill chunk at most 16, far below the 64-row tile of tcgen05.
+//      word w of piece f holds the 4 dims of one 16-dim MMA step (f, w), two per operand register;
+//   V: piece g (dims 16 g .. 16 g + 15) of 4 tokens per 16-token MMA step; a byte permute pairs two
+//      tokens' codes of one dim, which is what one operand register holds.
+// These are the warp-level MMAs (m16n8k16): a decode step has one query row per (sequence, head),
+// and an item of a prefill chunk at most 16, far below the 64-row tile of tcgen05; the products
+// are a small part of the time, the point is to take the dot products and their reductions off the
+// FMA pipes.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -57,31 +54,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-// d += A (16 x 32, row) * B (32 x 8, col); e4m3 operands, fp32 accumulators.
-__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four numbers (|x| <= 448, or NaN) to packed e4m3 codes, and what is left of them times 32.
-__device__ __forceinline__ uint32_t e4m3_term(float (&x)[4]) {
-    uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(x[1]), "f"(x[0]));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(x[3]), "f"(x[2]));
-    const uint32_t l = e4m3x2_to_f16x2(lo), h = e4m3x2_to_f16x2(hi);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&l));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    x[0] = (x[0] - a.x) * 32.f;
-    x[1] = (x[1] - a.y) * 32.f;
-    x[2] = (x[2] - b.x) * 32.f;
-    x[3] = (x[3] - b.y) * 32.f;
-    return (uint32_t)lo | (uint32_t)hi << 16;
-}
-
 // d += A (16 x 16, row) * B (16 x 8, col); fp16 operands, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
@@ -91,15 +63,31 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same into fresh accumulators.
+__device__ __forceinline__ void mma_f16_new(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                            uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 
-// The power of two that brings a row with largest magnitude amax into [2^kTop, 2^(kTop + 1)), and
-// its inverse.
-template <int kTop>
-__device__ __forceinline__ float row_scale(float amax, float &inverse) {
+// The power of two that brings a row with largest magnitude amax into [2^14, 2^15), and its
+// inverse.  A bf16 query times it is an fp16 number exactly down to 2^-28 of the row's largest
+// element (below that fp16's subnormals round it, by less than 2^-39 of the largest).
+__device__ __forceinline__ float f16_row_scale(float amax, float &inverse) {
     const int e = (int)(__float_as_uint(amax) >> 23) - 127;       // amax >= 0; 128 for inf / NaN
-    const int k = min(kTop - e, 126);                             // at least kTop - 128
+    const int k = min(14 - e, 126);                               // -114 .. 126
     inverse = __uint_as_float((uint32_t)(127 - k) << 23);
     return __uint_as_float((uint32_t)(127 + k) << 23);
+}
+
+// 2^x to 2 units; 0 below 2^-126.
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Word w (0..3) of a 16-byte piece.
@@ -129,43 +117,29 @@ __device__ __forceinline__ void mask_v8(uint4 (&v)[8], int visible, int lane) {
         if (4 * x + (lane & 3) >= visible) v[x] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// One decode query as the B operand of S^T = K q: columns 0..2 hold its terms, the rest zeros.
+// One decode query as the B operand of S^T = K q: column 0 holds the query, the rest zeros.  Its 16
+// registers a lane are read from shared memory at each tile (four 16-byte loads): lane c of the
+// first quad reads its dims, every other lane zeros.
 struct __align__(16) Query8Smem {
-    uint32_t t[4][kD / 4];   // terms 0..2, then zeros
+    uint2 x[kD / 4];     // fp16, dims 4 i .. 4 i + 3
+    uint2 zero[kD / 4];
 };
 struct Query8 {
-    uint4 w[2];      // dims 16 c .. + 15 and 64 + 16 c .. + 15 of term g
-    float unit;      // the products are in units of this
+    const uint4 *f;      // pieces 0, 1: dims 16 c .. + 15; pieces 8, 9: dims 64 + 16 c .. + 15
+    float unit;          // the products are in units of this
 };
 // By a whole warp, through an area of its own; raw: the lane's dims 4 lane .. 4 lane + 3.
 __device__ __forceinline__ Query8 split_query8(Query8Smem &sm, uint2 raw, int lane) {
-    float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
-                  __uint_as_float(raw.y & 0xffff0000u)};
+    const float x[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16),
+                        __uint_as_float(raw.y & 0xffff0000u)};
     const float amax = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
     Query8 q;
-    const float s = row_scale<7>(amax, q.unit);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] *= s;
-    // an infinity saturates in the first term and leaves one to the next: make it NaN there
-    bool fine = true;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) fine = fine && fabsf(x[e]) <= 448.f;
-    const uint32_t first = e4m3_term(x);
-    sm.t[0][lane] = fine ? first : 0x7f7f7f7fu;
-    sm.t[1][lane] = e4m3_term(x);
-    sm.t[2][lane] = e4m3_term(x);
-    sm.t[3][lane] = 0u;
+    const float s = f16_row_scale(amax, q.unit);
+    sm.x[lane] = make_uint2(pack_f16(x[0] * s, x[1] * s), pack_f16(x[2] * s, x[3] * s));
+    sm.zero[lane] = make_uint2(0u, 0u);
     __syncwarp();
-    const uint4 *src = reinterpret_cast<const uint4 *>(sm.t[min(lane >> 2, 3)]);
-    q.w[0] = src[lane & 3];
-    q.w[1] = src[4 + (lane & 3)];
+    q.f = reinterpret_cast<const uint4 *>(lane < 4 ? sm.x : sm.zero) + 2 * (lane & 3);
     return q;
-}
-
-// What a lane's two accumulator columns count for: columns 0, 1, 2 in units of 1, 2^-5, 2^-10.
-__device__ __forceinline__ float2 term_units(int lane) {
-    const int c = lane & 3;
-    return make_float2(c == 0 ? 1.f : c == 1 ? 1.f / 1024.f : 0.f, c == 0 ? 1.f / 32.f : 0.f);
 }
 
 // Scores of a K tile, in units of q.unit * scale: every lane of quad g gets those of tokens g, 8 + g,
@@ -173,64 +147,77 @@ __device__ __forceinline__ float2 term_units(int lane) {
 __device__ __forceinline__ void scores8(float (&z)[4], const uint4 (&k)[8], const Query8 &q, int lane) {
     float d[2][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m) d[m][0] = d[m][1] = d[m][2] = d[m][3] = 0.f;
+    for (int x = 0; x < 4; ++x) {
+        const uint4 b = q.f[8 * (x >> 1) + (x & 1)];   // MMA steps (x / 2, 2 (x % 2)) and the next
 #pragma unroll
-    for (int f = 0; f < 2; ++f)
+        for (int y = 0; y < 2; ++y)
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const uint4 &a = k[4 * m + f], &b = k[4 * m + 2 + f];
-            mma_e4m3(d[m], a.x, b.x, a.y, b.y, q.w[f].x, q.w[f].y);
-            mma_e4m3(d[m], a.z, b.z, a.w, b.w, q.w[f].z, q.w[f].w);
-        }
-    const float2 u = term_units(lane);
+            for (int m = 0; m < 2; ++m) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4_to_f16(word(k[4 * m + (x >> 1)], 2 * (x & 1) + y), a0, a2);
+                e4m3x4_to_f16(word(k[4 * m + 2 + (x >> 1)], 2 * (x & 1) + y), a1, a3);
+                if (x == 0 && y == 0)
+                    mma_f16_new(d[m], a0, a1, a2, a3, b.x, b.y);
+                else
+                    mma_f16(d[m], a0, a1, a2, a3, y ? b.z : b.x, y ? b.w : b.y);
+            }
+    }
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            // lanes c >= 2 hold columns of zeros
-            float t = (lane & 2) ? 0.f : fmaf(d[m][2 * y], u.x, d[m][2 * y + 1] * u.y);
-            t += __shfl_xor_sync(0xffffffffu, t, 1);
-            z[2 * m + y] = t + __shfl_xor_sync(0xffffffffu, t, 2);
-        }
+    for (int m = 0; m < 2; ++m) {
+        // column 0 sits in the lanes with c = 0
+        z[2 * m] = __shfl_sync(0xffffffffu, d[m][0], lane & 28);
+        z[2 * m + 1] = __shfl_sync(0xffffffffu, d[m][2], lane & 28);
+    }
 }
 
-// Four words (tokens), bytes = dims, to four words (dims), bytes = tokens.
-__device__ __forceinline__ void transpose4(uint32_t (&r)[4], uint32_t w0, uint32_t w1, uint32_t w2, uint32_t w3) {
-    const uint32_t a = __byte_perm(w0, w1, 0x5140), b = __byte_perm(w2, w3, 0x5140);
-    const uint32_t c = __byte_perm(w0, w1, 0x7362), d = __byte_perm(w2, w3, 0x7362);
-    r[0] = __byte_perm(a, b, 0x5410);
-    r[1] = __byte_perm(a, b, 0x7632);
-    r[2] = __byte_perm(c, d, 0x5410);
-    r[3] = __byte_perm(c, d, 0x7632);
-}
-
-// acc[e] += s * sum_t p_t v[t][16 g + e], for the weights p of scores8's tokens; the sum over the
-// lanes c = 0, 1 of a quad is the result.
+// acc[e] += s * sum_t p_t v[t][16 g + e] in the lanes with c = 0, for the weights p of scores8's
+// tokens.
 __device__ __forceinline__ void weighted_sum8(float (&acc)[16], const float (&p)[4], const uint4 (&v)[8], float s,
                                               int lane) {
     const int g = lane >> 2, c = lane & 3;
-    float x[4] = {p[0] * 256.f, p[1] * 256.f, p[2] * 256.f, p[3] * 256.f};
-    const uint32_t t0 = e4m3_term(x), t1 = e4m3_term(x), t2 = e4m3_term(x);
-    const uint32_t mine = c == 0 ? t0 : c == 1 ? t1 : c == 2 ? t2 : 0u;
-    // column g: term g of quads c (tokens c + 8 i) and c + 4
-    uint32_t b0 = __shfl_sync(0xffffffffu, mine, 4 * c + (g & 3));
-    uint32_t b1 = __shfl_sync(0xffffffffu, mine, 4 * c + (g & 3) + 16);
-    if (g >= 4) b0 = b1 = 0u;
-    const float2 u = term_units(lane);
-    const float s0 = s * (u.x * (1.f / 256.f)), s1 = s * (u.y * (1.f / 256.f));
+    uint32_t x01, x23;
+    {
+        const __half2 h01 = __floats2half2_rn(p[0], p[1]), h23 = __floats2half2_rn(p[2], p[3]);
+        const uint32_t l01 = pack_f16(p[0] - __low2float(h01), p[1] - __high2float(h01));
+        const uint32_t l23 = pack_f16(p[2] - __low2float(h23), p[3] - __high2float(h23));
+        x01 = c & 1 ? l01 : *reinterpret_cast<const uint32_t *>(&h01);
+        x23 = c & 1 ? l23 : *reinterpret_cast<const uint32_t *>(&h23);
+    }
+    const int src = 4 * c + (g & 1);
+    uint32_t b[2][2];
+    b[0][0] = __shfl_sync(0xffffffffu, x01, src);         // tokens c, c + 8
+    b[0][1] = __shfl_sync(0xffffffffu, x01, src + 16);    // tokens c + 4, c + 12
+    b[1][0] = __shfl_sync(0xffffffffu, x23, src);         // the same + 16
+    b[1][1] = __shfl_sync(0xffffffffu, x23, src + 16);
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {   // dims 4 w .. + 3 (rows g) and 8 + 4 w .. + 3 (rows g + 8)
-        uint32_t a0[4], a1[4], a2[4], a3[4];
-        transpose4(a0, word(v[0], w), word(v[2], w), word(v[4], w), word(v[6], w));
-        transpose4(a1, word(v[0], w + 2), word(v[2], w + 2), word(v[4], w + 2), word(v[6], w + 2));
-        transpose4(a2, word(v[1], w), word(v[3], w), word(v[5], w), word(v[7], w));
-        transpose4(a3, word(v[1], w + 2), word(v[3], w + 2), word(v[5], w + 2), word(v[7], w + 2));
+    for (int k = 0; k < 2; ++k)
+        if (g >= 2) b[k][0] = b[k][1] = 0u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4m3(d, a0[e], a1[e], a2[e], a3[e], b0, b1);
-            acc[4 * w + e] = fmaf(d[0], s0, fmaf(d[1], s1, acc[4 * w + e]));
-            acc[8 + 4 * w + e] = fmaf(d[2], s0, fmaf(d[3], s1, acc[8 + 4 * w + e]));
+    for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // dims 4 w + 2 half, + 1 (rows g) and + 8 (rows g + 8)
+            float d0[4], d1[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint32_t sel = half ? 0x7362u : 0x5140u;
+                uint32_t a0[2], a1[2], a2[2], a3[2];
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k], w), word(v[4 * k + 2], w), sel), a0[0], a0[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k], w + 2), word(v[4 * k + 2], w + 2), sel), a1[0], a1[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k + 1], w), word(v[4 * k + 3], w), sel), a2[0], a2[1]);
+                e4m3x4_to_f16(__byte_perm(word(v[4 * k + 1], w + 2), word(v[4 * k + 3], w + 2), sel), a3[0], a3[1]);
+                if (k == 0) {
+                    mma_f16_new(d0, a0[0], a1[0], a2[0], a3[0], b[0][0], b[0][1]);
+                    mma_f16_new(d1, a0[1], a1[1], a2[1], a3[1], b[0][0], b[0][1]);
+                } else {
+                    mma_f16(d0, a0[0], a1[0], a2[0], a3[0], b[1][0], b[1][1]);
+                    mma_f16(d1, a0[1], a1[1], a2[1], a3[1], b[1][0], b[1][1]);
+                }
+            }
+            const int e = 4 * w + 2 * half;
+            acc[e] = fmaf(s, d0[0] + d0[1], acc[e]);
+            acc[e + 8] = fmaf(s, d0[2] + d0[3], acc[e + 8]);
+            acc[e + 1] = fmaf(s, d1[0] + d1[1], acc[e + 1]);
+            acc[e + 9] = fmaf(s, d1[2] + d1[3], acc[e + 9]);
         }
     }
 }

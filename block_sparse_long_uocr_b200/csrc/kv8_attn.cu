@@ -16,8 +16,7 @@ namespace uocr {
 
 namespace {
 
-// A warp's softmax state over one or more blocks: the sum of acc over the lanes c = 0, 1 of quad g
-// holds dims 16 g .. 16 g + 15.
+// A warp's softmax state over one or more blocks: acc of lane (g, 0) holds dims 16 g .. 16 g + 15.
 struct State8 {
     float m = -INFINITY, l = 0.f;
     float acc[16];
@@ -74,11 +73,11 @@ __device__ __forceinline__ void attend8(State8 &st, const Blocks8 &bl, const uin
         for (int x = 4; x < 32; x <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
         const float m = fmaxf(st.m, mb);
         const float base = m == -INFINITY ? 0.f : m;      // every score -inf: weights 0, not NaN
-        const float corr = exp2f(st.m - base);            // 0 on the first block
+        const float corr = exp2_approx(st.m - base);            // 0 on the first block
         float w[4], lb = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = exp2f(z[i] - base);
+            w[i] = exp2_approx(z[i] - base);
             lb += w[i];
         }
 #pragma unroll
@@ -101,13 +100,11 @@ struct Merge8 {
 template <int kWarps>
 __device__ __forceinline__ void put_state8(Merge8<kWarps> &s, const State8 &st, int warp, int lane) {
     if (lane == 0) s.ml[warp] = make_float2(st.m, st.l);
-    float a[16];
-#pragma unroll
-    for (int e = 0; e < 16; ++e) a[e] = st.acc[e] + __shfl_xor_sync(0xffffffffu, st.acc[e], 1);
     if ((lane & 3) == 0) {
         float4 *dst = reinterpret_cast<float4 *>(&s.acc[warp][16 * (lane >> 2)]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) dst[e] = make_float4(a[4 * e], a[4 * e + 1], a[4 * e + 2], a[4 * e + 3]);
+        for (int e = 0; e < 4; ++e)
+            dst[e] = make_float4(st.acc[4 * e], st.acc[4 * e + 1], st.acc[4 * e + 2], st.acc[4 * e + 3]);
     }
 }
 // The merged state, by threads d < 128 after a barrier: thread d gets dim d of the output.
