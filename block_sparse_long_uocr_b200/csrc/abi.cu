@@ -579,6 +579,7 @@ inline uocr_status_t check_seq_kv8(const void *q, const void *k_cache, const voi
     // units of work and block totals are counted in int32
     if ((long long)uocr::prefill_item_bound(n_q, max_blocks) * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;
     if ((long long)max_blocks * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;
+    if ((long long)num_pages * H > 0x7fffffffLL) return UOCR_ERR_UNSUPPORTED;   // TMA tile coordinates are int32
     return UOCR_OK;
 }
 }  // namespace

@@ -21,13 +21,16 @@
 // sum l keeps 32 bits) and the partial outputs to fp16 (2^-11; |acc| <= 32 * 448, in units of the
 // block's value scale, so fp16 holds it): each an eighth of the output's own rounding to bf16.
 //
-// Staging of step 3.  A lane's operand registers are whole 16-byte pieces of K, V and Q rows, so each
-// lane copies its own 24 pieces into its own place in shared memory with cp.async and reads them
-// back: no lane reads what another wrote, so there is no barrier, no swizzle and no bank conflict,
-// only a queue that costs no registers.  The next unit's K and Q start once this unit's S is done, its
-// V once P V is; its entries are loaded one unit ahead and its record two, so that a unit waits for
-// one memory latency at most.
+// Staging of step 3, per warp: a K tile and a V tile by TMA in the 128-byte swizzle (16-byte piece p
+// of row r at p ^ (r & 7)), and the item's query rows by one bulk copy each, 320 bytes apart.  The next
+// unit's K and Q start once this unit's S is done, its V once P V is; its entries are loaded one unit
+// ahead and its record two, so that a unit waits for one memory latency at most.  Bank conflicts: an
+// 8-lane phase of a 16-byte read covers two MMA columns (or rows) g = 2 m, 2 m + 1 and four pieces, so
+// column g of K stands for token rho(g) = 4 (g & 1) + g / 2 of its 8 (the two rows then differ in bit 2
+// of the swizzle), V's rows c + 4 y are read in the order y ^ (c & 1), put right by the selector of the
+// byte permute that pairs them, and neighbouring query rows start 64 bytes of banks apart.
 #include <math.h>
+#include <stddef.h>
 
 #include "kernels.h"
 #include "kv8.cuh"
@@ -40,9 +43,11 @@ constexpr int kBlkWarps = 4, kBlkCtas = 4;
 constexpr int kMrgWarps = 8;
 constexpr float kMassUnit = 1.f / (1ll << 40);
 
-// A warp's queue: piece x of lane l at x * 32 + l.
-struct UnitSmem {
-    uint4 k[8 * 32], v[8 * 32], q[8 * 32];
+constexpr int kQStride = kD * 2 + 64;
+
+struct __align__(1024) UnitSmem {
+    uint8_t k[kTile8], v[kTile8];
+    uint8_t q[kRows * kQStride];
 };
 
 // Four codes to fp16 where it stands in the program: moved ahead, the conversions of a whole tile
@@ -52,20 +57,34 @@ __device__ __forceinline__ void to_f16_here(uint32_t v, uint32_t &lo, uint32_t &
                  : "=r"(lo), "=r"(hi)
                  : "r"(v));
 }
-template <int kDst>
-__device__ __forceinline__ void cp_async16(uint32_t dst, const uint4 *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + kDst), "l"(src) : "memory");
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap *map, int tile, uint64_t *bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %2, "
+        "%3}], [%4], %5;" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(tile), "r"(smem_addr(bar)), "l"(policy)
+        : "memory");
 }
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kPending>
-__device__ __forceinline__ void cp_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+__device__ __forceinline__ void bulk_row(uint32_t dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_smem(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
 }
 // Stores that stay in L2 for the merge of the same call.
 __device__ __forceinline__ void st_keep(uint4 *p, const uint4 &v, uint64_t policy) {
     asm volatile("st.global.L2::cache_hint.v4.b32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w), "l"(policy)
                  : "memory");
+}
+// A load that is issued where it stands, so that a row's 16 are in flight together.
+__device__ __forceinline__ uint4 ld_l2(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
 }
 __device__ __forceinline__ void discard_line(const void *p) {   // 128 bytes, not written back
     asm volatile("discard.global.L2 [%0], 128;" ::"l"(p) : "memory");
@@ -118,17 +137,33 @@ kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel,
 }
 
 __global__ void __launch_bounds__(kBlkWarps * 32, kBlkCtas)
-kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, const uint4 *__restrict__ kc,
-                 const uint4 *__restrict__ vc, const float *__restrict__ k_scale, const float *__restrict__ v_scale,
-                 const int2 *__restrict__ list, const int4 *__restrict__ items, const int32_t *__restrict__ n_items,
+kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                 const uint4 *__restrict__ q16, const float *__restrict__ unit, const float *__restrict__ k_scale,
+                 const float *__restrict__ v_scale, const int2 *__restrict__ list, const int4 *__restrict__ items, const int32_t *__restrict__ n_items,
                  int H, int num_pages, float scale_log2, uint4 *__restrict__ part_o, float4 *__restrict__ part_ml,
                  int32_t *dev_err) {
-    __shared__ UnitSmem sm[kBlkWarps];
+    extern __shared__ uint8_t raw_smem[];
+    __shared__ uint64_t s_bar[kBlkWarps][2];   // K and Q, V of the warp's unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const uint4 *sk = sm[warp].k + lane, *sv = sm[warp].v + lane, *sq = sm[warp].q + lane;
-    const uint32_t ak = smem_addr(sk), av = smem_addr(sv), aq = smem_addr(sq);
-    uint64_t keep;
+    uint64_t *bar_k = &s_bar[warp][0], *bar_v = &s_bar[warp][1];
+    const uint32_t area = ((smem_addr(raw_smem) + 1023u) & ~1023u) + warp * (uint32_t)sizeof(UnitSmem);
+    const uint32_t at_k = area + offsetof(UnitSmem, k), at_v = area + offsetof(UnitSmem, v);
+    const uint32_t at_q = area + offsetof(UnitSmem, q);
+    // this lane's pieces: K piece c of row rho(g) of an 8-row group (piece c + 4 is 64 bytes away by xor,
+    // the next group 1024 bytes on); V piece g of row r0 (row r0 ^ 4: by xor); Q piece c of row g
+    const int rho = ((g & 1) << 2) | (g >> 1), r0 = c + 4 * (c & 1);
+    const uint32_t my_k = at_k + rho * kD + ((c ^ rho) << 4);
+    const uint32_t my_v = at_v + r0 * kD + ((g ^ r0) << 4);
+    const uint32_t my_q = at_q + g * kQStride + (c << 4);
+    if (lane == 0) {
+        mbar_init(bar_k, 1);
+        mbar_init(bar_v, 1);
+        fence_mbar_init();
+    }
+    __syncwarp();
+    uint64_t keep, once;
     asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
     pdl_wait();
 
     // Units (item, head), heads innermost, dealt round-robin over the warps: unit u is (item, h), the
@@ -156,46 +191,26 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
     };
     auto page_ok = [&](const int4 &rec) { return (unsigned)rec.y < (unsigned)num_pages; };
     auto issue_qk = [&](const int4 &rec, int h, int2 ea, int2 eb) {
-        if (page_ok(rec)) {
-            const uint4 *src = kc + ((size_t)rec.y * H + h) * kTile8U4 + g * kRowU4 + c;
-            cp_async16<0 * 512>(ak, src);
-            cp_async16<1 * 512>(ak, src + 4);
-            cp_async16<2 * 512>(ak, src + 8 * kRowU4);
-            cp_async16<3 * 512>(ak, src + 8 * kRowU4 + 4);
-            cp_async16<4 * 512>(ak, src + 16 * kRowU4);
-            cp_async16<5 * 512>(ak, src + 16 * kRowU4 + 4);
-            cp_async16<6 * 512>(ak, src + 24 * kRowU4);
-            cp_async16<7 * 512>(ak, src + 24 * kRowU4 + 4);
-            // rows g and g + 8
-            const uint4 *qa = q16 + ((size_t)(ea.x >> 4) * H + h) * 16 + c;
-            const uint4 *qb = q16 + ((size_t)(eb.x >> 4) * H + h) * 16 + c;
-            cp_async16<0 * 512>(aq, qa);
-            cp_async16<1 * 512>(aq, qa + 4);
-            cp_async16<2 * 512>(aq, qa + 8);
-            cp_async16<3 * 512>(aq, qa + 12);
-            cp_async16<4 * 512>(aq, qb);
-            cp_async16<5 * 512>(aq, qb + 4);
-            cp_async16<6 * 512>(aq, qb + 8);
-            cp_async16<7 * 512>(aq, qb + 12);
+        if (!page_ok(rec)) return;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar_k, kTile8 + rec.w * (kD * 2));
+            tma_tile(at_k, &map_k, rec.y * H + h, bar_k, once);
         }
-        cp_commit();
+        __syncwarp();
+        // row r by lane 4 (r & 7) + r / 8 (it has the entry); rows past the item's end are left as they
+        // are: what is computed from them is not stored
+        const int row = g + 8 * c;
+        if (c < 2 && row < rec.w)
+            bulk_row(at_q + row * kQStride, q16 + ((size_t)((c ? eb.x : ea.x) >> 4) * H + h) * 16, kD * 2, bar_k);
     };
-    // v piece 4 s + j: piece g of token 16 s + 8 (j / 2) + 2 c + j % 2, so that P's accumulator layout is
-    // the operand's
     auto issue_v = [&](const int4 &rec, int h) {
-        if (page_ok(rec)) {
-            const uint4 *src = vc + ((size_t)rec.y * H + h) * kTile8U4 + 2 * c * kRowU4 + g;
-            cp_async16<0 * 512>(av, src);
-            cp_async16<1 * 512>(av, src + kRowU4);
-            cp_async16<2 * 512>(av, src + 8 * kRowU4);
-            cp_async16<3 * 512>(av, src + 9 * kRowU4);
-            cp_async16<4 * 512>(av, src + 16 * kRowU4);
-            cp_async16<5 * 512>(av, src + 17 * kRowU4);
-            cp_async16<6 * 512>(av, src + 24 * kRowU4);
-            cp_async16<7 * 512>(av, src + 25 * kRowU4);
+        if (page_ok(rec) && lane == 0) {
+            mbar_arrive_expect_tx(bar_v, kTile8);
+            tma_tile(at_v, &map_v, rec.y * H + h, bar_v, once);
         }
-        cp_commit();
     };
+    uint32_t parity = 0;
+    bool dead = false;   // a wait ran out: what follows is left empty
 
     const int first = blockIdx.x * kBlkWarps + warp;
     Place at{first / H, first % H};
@@ -212,7 +227,7 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
     while (rec.w > 0) {
         const int h = at.h;
         const int row_a = (ea.x >> 4) * H + h, row_b = (eb.x >> 4) * H + h;   // below 2^30
-        const bool good = page_ok(rec);
+        const bool good = page_ok(rec) && !dead;
         float vs = 0.f, ks = 0.f, ua = 0.f, ub = 0.f;
         if (good) {
             const size_t tile = (size_t)rec.y * H + h;
@@ -220,21 +235,22 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
             vs = __ldg(v_scale + tile);
             ua = __ldcg(unit + row_a);
             ub = __ldcg(unit + row_b);
-        } else if (lane == 0) {
+        } else if (lane == 0 && !dead) {
             flag_error(dev_err, UOCR_DEVERR_PAGE);
         }
 
-        // ---- S: rows g, g + 8; tokens 8 nt + 2 c, + 1
-        cp_wait<1>();
+        // ---- S: rows g, g + 8; tokens 8 nt + c, 8 nt + 4 + c
+        bool ok = !good || mbar_wait_timed(bar_k, parity, kWaitLimitNs, nullptr);
+        __syncwarp();
         float s[4][4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
             uint4 k[4];
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt) k[nt] = sk[32 * (2 * nt + f)];
+            for (int nt = 0; nt < 4; ++nt) k[nt] = ld_smem((my_k ^ (64u * f)) + 1024u * nt);
 #pragma unroll
             for (int y = 0; y < 2; ++y) {
-                const uint4 a = sq[32 * (2 * f + y)], b = sq[32 * (4 + 2 * f + y)];
+                const uint4 a = ld_smem(my_q + 64u * (2 * f + y)), b = ld_smem(my_q + 8 * kQStride + 64u * (2 * f + y));
 #pragma unroll
                 for (int nt = 0; nt < 4; ++nt) {
                     uint32_t b0, b1;
@@ -248,7 +264,8 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
                 }
             }
         }
-        issue_qk(rec1, at1.h, ea1, eb1);   // K and Q are in registers or used
+        __syncwarp();   // K and Q are read: the next unit's may land
+        if (!dead) issue_qk(rec1, at1.h, ea1, eb1);
 
         // ---- causal mask, maxima, weights
         const int t0 = rec.x * kBlock;
@@ -267,7 +284,7 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = t0 + 8 * nt + 2 * c + e;
+                    const int tok = t0 + 8 * nt + 4 * e + c;
                     if (tok > ea.y) s[nt][e] = -INFINITY;
                     if (tok > eb.y) s[nt][2 + e] = -INFINITY;
                 }
@@ -303,8 +320,11 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
         }
 
         // ---- O = P V8: rows g, g + 8; column n of MMA e is dim 16 n + e
-        cp_wait<1>();
-        auto v_token = [&](int x) { return 16 * (x >> 2) + 8 * ((x >> 1) & 1) + 2 * c + (x & 1); };
+        ok = (!good || mbar_wait_timed(bar_v, parity, kWaitLimitNs, nullptr)) && ok;
+        ok = __all_sync(0xffffffffu, ok);
+        if (good) parity ^= 1;
+        auto v_token = [&](int x) { return 8 * (x >> 1) + (x & 1 ? r0 ^ 4 : r0); };
+        auto v_piece = [&](int x) { return ld_smem((x & 1 ? my_v ^ (4u * kD + 64u) : my_v) + 1024u * (x >> 1)); };
         // A token behind a query's position has weight 0, but 0 * NaN is not 0.  Tokens that no query
         // of the item sees may hold anything and are cut off for all of them; where some queries see
         // a token that others do not and its value is NaN, each row gets a product of its own.
@@ -313,13 +333,14 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
             uint32_t nan = 0u;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                const uint4 v = sv[32 * x];
+                const uint4 v = v_piece(x);
                 if (v_token(x) < far)
 #pragma unroll
                     for (int w = 0; w < 4; ++w) nan |= __vcmpeq4(word(v, w) & 0x7f7f7f7fu, 0x7f7f7f7fu);
             }
             apart = __any_sync(0xffffffffu, nan != 0u);
         }
+        const uint32_t sel_lo = c & 1 ? 0x1504u : 0x5140u, sel_hi = c & 1 ? 0x3726u : 0x7362u;
 #pragma unroll 1
         for (int turn = 0; turn < (apart ? kRows : 1); ++turn) {
             int seen = far;
@@ -329,10 +350,13 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
                 want_a = want_a && turn == g;
                 want_b = want_b && turn == g + 8;
             }
-            uint32_t oa[2][8], ob[2][8];   // fp16 pairs of dims 32 c + 16 half + 2 i, + 1
+            // piece 4 w4 + c of a partial holds dims 32 c + 4 w4 .. + 3 and 32 c + 16 + 4 w4 .. + 3: what a
+            // lane has at one step, so that a row's four lanes write 64 bytes together
+            uint4 *dst_a = part_o + ((size_t)row_a * kSel + (ea.x & 15)) * 16 + c;
+            uint4 *dst_b = part_o + ((size_t)row_b * kSel + (eb.x & 15)) * 16 + c;
             uint4 v[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) v[x] = sv[32 * x];
+            for (int x = 0; x < 8; ++x) v[x] = v_piece(x);
             if (seen < kBlock) {
 #pragma unroll
                 for (int x = 0; x < 8; ++x)
@@ -346,10 +370,10 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
                     uint32_t b0[4], b1[4];
                     const uint32_t t0w = word(v[4 * kk], w4), t1w = word(v[4 * kk + 1], w4);
                     const uint32_t t2w = word(v[4 * kk + 2], w4), t3w = word(v[4 * kk + 3], w4);
-                    to_f16_here(__byte_perm(t0w, t1w, 0x5140), b0[0], b0[1]);
-                    to_f16_here(__byte_perm(t0w, t1w, 0x7362), b0[2], b0[3]);
-                    to_f16_here(__byte_perm(t2w, t3w, 0x5140), b1[0], b1[1]);
-                    to_f16_here(__byte_perm(t2w, t3w, 0x7362), b1[2], b1[3]);
+                    to_f16_here(__byte_perm(t0w, t1w, sel_lo), b0[0], b0[1]);
+                    to_f16_here(__byte_perm(t0w, t1w, sel_hi), b0[2], b0[3]);
+                    to_f16_here(__byte_perm(t2w, t3w, sel_lo), b1[0], b1[1]);
+                    to_f16_here(__byte_perm(t2w, t3w, sel_hi), b1[2], b1[3]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         if (kk == 0)
@@ -358,36 +382,27 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
                             mma_f16(o[e], pa[2], pb[2], pa[3], pb[3], b0[e], b1[e]);
                     }
                 }
-#pragma unroll
-                for (int half = 0; half < 2; ++half)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        oa[half][2 * w4 + e] = pack_f16(o[2 * e][half], o[2 * e + 1][half]);
-                        ob[half][2 * w4 + e] = pack_f16(o[2 * e][2 + half], o[2 * e + 1][2 + half]);
-                    }
-            }
-            if (want_a) {
-                uint4 *dst = part_o + ((size_t)row_a * kSel + (ea.x & 15)) * 16 + 4 * c;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    st_keep(dst + x, make_uint4(oa[x >> 1][4 * (x & 1)], oa[x >> 1][4 * (x & 1) + 1],
-                                                oa[x >> 1][4 * (x & 1) + 2], oa[x >> 1][4 * (x & 1) + 3]), keep);
-            }
-            if (want_b) {
-                uint4 *dst = part_o + ((size_t)row_b * kSel + (eb.x & 15)) * 16 + 4 * c;
-#pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    st_keep(dst + x, make_uint4(ob[x >> 1][4 * (x & 1)], ob[x >> 1][4 * (x & 1) + 1],
-                                                ob[x >> 1][4 * (x & 1) + 2], ob[x >> 1][4 * (x & 1) + 3]), keep);
+                if (want_a)
+                    st_keep(dst_a + 4 * w4, make_uint4(pack_f16(o[0][0], o[1][0]), pack_f16(o[2][0], o[3][0]),
+                                                       pack_f16(o[0][1], o[1][1]), pack_f16(o[2][1], o[3][1])), keep);
+                if (want_b)
+                    st_keep(dst_b + 4 * w4, make_uint4(pack_f16(o[0][2], o[1][2]), pack_f16(o[2][2], o[3][2]),
+                                                       pack_f16(o[0][3], o[1][3]), pack_f16(o[2][3], o[3][3])), keep);
             }
         }
-        issue_v(rec1, at1.h);   // V is in registers or used
+        __syncwarp();   // V is read: the next unit's may land
+        if (!ok) {      // a copy did not arrive in time: nothing of this unit and of those after it is kept
+            if (lane == 0 && !dead) flag_error(dev_err, UOCR_DEVERR_TIMEOUT);
+            dead = true;
+        }
+        if (!dead) issue_v(rec1, at1.h);
 
-        if (c == 0) {   // (a page outside the pool: nothing was copied, the state is empty)
+        const bool full = good && ok;   // else (also: a page outside the pool) the states are empty
+        if (c == 0) {
             if (g < rec.w)
-                part_ml[(size_t)row_a * kSel + (ea.x & 15)] = make_float4(good ? ma : -INFINITY, good ? la : 0.f, vs, 0.f);
+                part_ml[(size_t)row_a * kSel + (ea.x & 15)] = make_float4(full ? ma : -INFINITY, full ? la : 0.f, vs, 0.f);
             if (g + 8 < rec.w)
-                part_ml[(size_t)row_b * kSel + (eb.x & 15)] = make_float4(good ? mb : -INFINITY, good ? lb : 0.f, vs, 0.f);
+                part_ml[(size_t)row_b * kSel + (eb.x & 15)] = make_float4(full ? mb : -INFINITY, full ? lb : 0.f, vs, 0.f);
         }
         at = at1;
         rec = rec1;
@@ -400,7 +415,10 @@ kv8_block_kernel(const uint4 *__restrict__ q16, const float *__restrict__ unit, 
         at2 = advance(at2);
         rec2 = load_rec(at2);
     }
-    cp_wait<0>();
+    if (dead) {   // copies still on their way end before the shared memory goes
+        mbar_drain(bar_k, parity, dev_err);
+        mbar_drain(bar_v, parity ^ 1, dev_err);
+    }
 }
 
 __global__ void __launch_bounds__(kMrgWarps * 32)
@@ -434,7 +452,8 @@ kv8_merge_kernel(const int32_t *__restrict__ sel_ws, const uint4 *__restrict__ p
 #pragma unroll
     for (int s = 0; s < kSel; ++s) {
         const bool has = __shfl_sync(0xffffffffu, (int)some, s, 16);
-        v[s] = has ? __ldcg(part_o + (slot + s) * 16 + k) : make_uint4(0u, 0u, 0u, 0u);
+        v[s] = make_uint4(0u, 0u, 0u, 0u);
+        if (has) v[s] = ld_l2(part_o + (slot + s) * 16 + k);
     }
 #pragma unroll
     for (int s = 0; s < kSel; ++s) {
@@ -464,7 +483,10 @@ kv8_merge_kernel(const int32_t *__restrict__ sel_ws, const uint4 *__restrict__ p
                                                 : __floats2bfloat162_rn(0.f, 0.f);
         r[e] = *reinterpret_cast<const uint32_t *>(&y);
     }
-    out[(size_t)ih * 16 + k] = make_uint4(r[0], r[1], r[2], r[3]);
+    // piece k = 4 w4 + c of a partial holds dims 32 c + 4 w4 .. + 3 and 32 c + 16 + 4 w4 .. + 3
+    uint2 *to = reinterpret_cast<uint2 *>(out + (size_t)ih * 16) + 8 * (k & 3) + (k >> 2);
+    to[0] = make_uint2(r[0], r[1]);
+    to[4] = make_uint2(r[2], r[3]);
     if (mass_fx && some) {
         const float share = finite_weight(w / L);   // in [0, 1]
         atomicAdd(mass_fx + (size_t)h * max_blocks + j, (unsigned long long)__float2ull_rn(share / kMassUnit));
@@ -513,6 +535,21 @@ Kv8PrefillWs layout(int n_q, int H, int max_blocks) {
 }
 }  // namespace
 
+namespace {
+// A cache of codes as a 3-D tensor (dim, token, page * H + head), read in boxes of one tile.
+bool tile8_map(CUtensorMap *map, const void *cache, int num_pages, int H) {
+    EncodeTiledFn enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)kBlock, (cuuint64_t)num_pages * H};
+    const cuuint64_t strides[2] = {(cuuint64_t)kD, (cuuint64_t)kTile8};
+    const cuuint32_t box[3] = {(cuuint32_t)kD, (cuuint32_t)kBlock, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(cache), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+}  // namespace
+
 size_t prefill_kv8_workspace(int n_q, int H, int max_blocks) { return layout(n_q, H, max_blocks).total; }
 
 cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, int32_t **sched) {
@@ -553,12 +590,19 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     if (e != cudaSuccess) return e;
 
     cfg.numAttrs = 1;
+    CUtensorMap map_k, map_v;
+    if (!tile8_map(&map_k, kv.k, num_pages, H) || !tile8_map(&map_v, kv.v, num_pages, H)) return cudaErrorInvalidValue;
+    constexpr int kSmem = kBlkWarps * (int)sizeof(UnitSmem) + 1024;
+    e = cudaFuncSetAttribute(kv8_block_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(kBlkCtas * c.num_sms));
     cfg.blockDim = dim3(kBlkWarps * 32);
-    e = cudaLaunchKernelEx(&cfg, kv8_block_kernel, (const uint4 *)q16, (const float *)unit, (const uint4 *)kv.k,
-                           (const uint4 *)kv.v, kv.k_scale, kv.v_scale, (const int2 *)list, (const int4 *)items,
-                           (const int32_t *)n_items, H, num_pages, scale * kLog2e, part_o, ml, dev_err);
+    cfg.dynamicSmemBytes = kSmem;
+    e = cudaLaunchKernelEx(&cfg, kv8_block_kernel, map_k, map_v, (const uint4 *)q16, (const float *)unit, kv.k_scale,
+                           kv.v_scale, (const int2 *)list, (const int4 *)items, (const int32_t *)n_items, H, num_pages,
+                           scale * kLog2e, part_o, ml, dev_err);
     if (e != cudaSuccess) return e;
+    cfg.dynamicSmemBytes = 0;
 
     const long long rows = (long long)n_q * H;
     cfg.gridDim = dim3((unsigned)((rows + 2 * kMrgWarps - 1) / (2 * kMrgWarps)));

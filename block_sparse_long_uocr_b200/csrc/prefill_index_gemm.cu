@@ -36,6 +36,8 @@
 #include <cuda_bf16.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
@@ -500,12 +502,17 @@ prefill_index_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __gri
 
 // ---------------------------------------------------------------- host side
 EncodeTiledFn tensor_map_encoder() {
+    static std::atomic<EncodeTiledFn> found{nullptr};   // looked up until it is found, then kept
+    EncodeTiledFn fn = found.load(std::memory_order_acquire);
+    if (fn) return fn;
     void *p = nullptr;
     cudaDriverEntryPointQueryResult q;
     if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
         q != cudaDriverEntryPointSuccess)
         return nullptr;
-    return reinterpret_cast<EncodeTiledFn>(p);
+    fn = reinterpret_cast<EncodeTiledFn>(p);
+    found.store(fn, std::memory_order_release);
+    return fn;
 }
 
 namespace {
