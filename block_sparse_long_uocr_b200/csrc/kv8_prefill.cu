@@ -81,9 +81,13 @@ __device__ __forceinline__ void st_keep(uint4 *p, const uint4 &v, uint64_t polic
                  : "memory");
 }
 // A load that is issued where it stands, so that a row's 16 are in flight together.
-__device__ __forceinline__ uint4 ld_l2(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+__device__ __forceinline__ uint4 ld_l2(const uint4 *p, bool wanted) {   // zeros where not wanted
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    asm volatile(
+        "{\n .reg .pred w;\n setp.ne.s32 w, %5, 0;\n @w ld.global.cg.v4.b32 {%0, %1, %2, %3}, [%4];\n}"
+        : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)
+        : "l"(p), "r"((int)wanted)
+        : "memory");
     return v;
 }
 __device__ __forceinline__ void discard_line(const void *p) {   // 128 bytes, not written back
@@ -97,6 +101,12 @@ kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel,
                    const int32_t *__restrict__ seq_len_ptr, int H, int max_blocks, int32_t *__restrict__ sel_ws,
                    int32_t *counts, uint4 *__restrict__ q16, float *__restrict__ unit, int32_t *dev_err) {
     const int i = blockIdx.x, tid = threadIdx.x;
+    // (No kernel here lets the next one start early: waiting CTAs hold room that the running ones' later
+    // CTAs need; 79 us became 85 to 88 for 2048 queries.)
+    // 16 lanes per (query, head) row, 8 dims each: the rows are inputs of the call, so the first round
+    // is on its way before the wait
+    const int l = tid & 15;
+    uint4 raw = (tid >> 4) < H ? __ldg(q + ((size_t)i * H + (tid >> 4)) * 16 + l) : make_uint4(0u, 0u, 0u, 0u);
     pdl_wait();
     if (tid < kSel) {
         const int len = __ldg(seq_len_ptr), p = __ldg(q_pos + i);
@@ -111,14 +121,13 @@ kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel,
         sel_ws[(size_t)i * kSel + tid] = j;
         if (j >= 0) atomicAdd(counts + j, 1);
     }
-    // 16 lanes per (query, head) row, 8 dims each
-    const int l = tid & 15;
     for (int h0 = 0; h0 < H; h0 += 8) {
         const int h = h0 + (tid >> 4);
         const bool live = h < H;
         float x[8];
         float amax = 0.f;
-        bf16x8_to_f32(live ? __ldg(q + ((size_t)i * H + h) * 16 + l) : make_uint4(0u, 0u, 0u, 0u), x);
+        bf16x8_to_f32(raw, x);
+        raw = h + 8 < H ? __ldg(q + ((size_t)i * H + h + 8) * 16 + l) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
@@ -271,22 +280,26 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         const int t0 = rec.x * kBlock;
         const int far = __reduce_max_sync(0xffffffffu, max(ea.y, eb.y)) - t0 + 1;
         const int near = __reduce_min_sync(0xffffffffu, min(ea.y, eb.y)) - t0 + 1;
+        // z = s fa (rows g), s fb: the maximum is taken over s, whose sign the factors then do not change,
+        // and each weight is one product and one exponential, 2^(s fa - ma)
         ks *= scale_log2;
+        if (ks < 0.f) {   // a negative scale
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+            for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s[nt][e] = s[nt][e] * ua * ks;
-                s[nt][2 + e] = s[nt][2 + e] * ub * ks;
-            }
-        if (near < kBlock) {   // some query does not see the whole block
+                for (int e = 0; e < 4; ++e) s[nt][e] = -s[nt][e];
+            ks = -ks;
+        }
+        const float fa = ua * ks, fb = ub * ks;
+        const bool partly = near < kBlock;   // some query does not see the whole block
+        auto hidden = [&](int nt, int e, int pos) { return t0 + 8 * nt + 4 * e + c > pos; };
+        if (partly) {
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = t0 + 8 * nt + 4 * e + c;
-                    if (tok > ea.y) s[nt][e] = -INFINITY;
-                    if (tok > eb.y) s[nt][2 + e] = -INFINITY;
+                    if (hidden(nt, e, ea.y)) s[nt][e] = -INFINITY;
+                    if (hidden(nt, e, eb.y)) s[nt][2 + e] = -INFINITY;
                 }
         }
         float ma = -INFINITY, mb = -INFINITY, la = 0.f, lb = 0.f;
@@ -302,16 +315,29 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, x));
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
         }
-        const float base_a = ma == -INFINITY ? 0.f : ma, base_b = mb == -INFINITY ? 0.f : mb;
+        // the states' units are 2^ma, 2^mb (every score NaN or -inf: 2^0, and the sums say which)
+        ma = ma == -INFINITY ? 0.f : ma * fa;
+        mb = mb == -INFINITY ? 0.f : mb * fb;
         uint32_t pa[4], pb[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
-            const float p0 = exp2_approx(s[nt][0] - base_a), p1 = exp2_approx(s[nt][1] - base_a);
-            const float p2 = exp2_approx(s[nt][2] - base_b), p3 = exp2_approx(s[nt][3] - base_b);
-            la += p0 + p1;
-            lb += p2 + p3;
-            pa[nt] = pack_f16(p0, p1);
-            pb[nt] = pack_f16(p2, p3);
+            float p[4];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                p[e] = exp2_approx(fmaf(s[nt][e], fa, -ma));
+                p[2 + e] = exp2_approx(fmaf(s[nt][2 + e], fb, -mb));
+            }
+            if (partly) {   // (-inf times a scale of 0 is not -inf)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (hidden(nt, e, ea.y)) p[e] = 0.f;
+                    if (hidden(nt, e, eb.y)) p[2 + e] = 0.f;
+                }
+            }
+            la += p[0] + p[1];
+            lb += p[2] + p[3];
+            pa[nt] = pack_f16(p[0], p[1]);
+            pb[nt] = pack_f16(p[2], p[3]);
         }
 #pragma unroll
         for (int x = 1; x < 4; x <<= 1) {
@@ -421,7 +447,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
     }
 }
 
-__global__ void __launch_bounds__(kMrgWarps * 32)
+__global__ void __launch_bounds__(kMrgWarps * 32, 2)
 kv8_merge_kernel(const int32_t *__restrict__ sel_ws, const uint4 *__restrict__ part_o,
                  const float4 *__restrict__ part_ml, int n_rows, int H, int max_blocks, uint4 *__restrict__ out,
                  unsigned long long *mass_fx) {
@@ -452,8 +478,7 @@ kv8_merge_kernel(const int32_t *__restrict__ sel_ws, const uint4 *__restrict__ p
 #pragma unroll
     for (int s = 0; s < kSel; ++s) {
         const bool has = __shfl_sync(0xffffffffu, (int)some, s, 16);
-        v[s] = make_uint4(0u, 0u, 0u, 0u);
-        if (has) v[s] = ld_l2(part_o + (slot + s) * 16 + k);
+        v[s] = ld_l2(part_o + (slot + s) * 16 + k, has);
     }
 #pragma unroll
     for (int s = 0; s < kSel; ++s) {
