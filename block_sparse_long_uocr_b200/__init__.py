@@ -608,14 +608,13 @@ def evict_workspace_bytes(n_seq: int, heads: int, max_blocks: int) -> int:
     return int(_lib().uocr_evict_workspace_bytes(int(n_seq), int(heads), int(max_blocks)))
 
 
-# The entry points below check their tensors on every call of a decode loop: `_fits` asks the four
-# things that matter as cheaply as Python can, and only when one is wrong does `_refuse` look for it
-# and say which (28 us per call of sparse_attn_kv8, its launch included, became 12.5).
+# The entry points below check their tensors on every call of a decode loop, so each asks in one
+# expression, without calls, what matters of each tensor: type, shape, device and density.  Only when
+# something is wrong does `_refuse` look for it and say which.  (Checks by function calls took 28 us per
+# call of sparse_attn_kv8, its launch included; a function per tensor 11.3, this 9.8.)
 _BF16, _F32, _I32, _E4M3, _U8 = torch.bfloat16, torch.float32, torch.int32, torch.float8_e4m3fn, torch.uint8
-
-
-def _fits(t, dtype, shape, dev: int) -> bool:
-    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+_WRONG = (AttributeError, TypeError, ValueError, IndexError)   # what looking at something else raises
+_SCALE = HEAD_DIM ** -0.5
 
 
 def _refuse(dev: int, *specs):
@@ -629,11 +628,10 @@ def _refuse(dev: int, *specs):
             raise ValueError(f"{name} must be on cuda:{dev} like the other tensors, got {t.device}")
 
 
-def _device_of(t, name: str, dtype, ndim: int) -> int:
-    """The device index of a call's leading tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.dim() != ndim or not t.is_cuda or not t.is_contiguous():
-        _dev(t, name, dtype, ndim)
-    return t.get_device()
+def _need(t, name: str):
+    if t is None:
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t
 
 
 def _at(t):
@@ -662,31 +660,19 @@ def _kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H):
             (k_scale, "k_scale", _F32, (P, H)), (v_scale, "v_scale", _F32, (P, H)))
 
 
-def _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev) -> bool:
-    tile, scale = (P, H, BLOCK, HEAD_DIM), (P, H)
-    return (_fits(k_cache, _E4M3, tile, dev) and _fits(v_cache, _E4M3, tile, dev) and _fits(k_scale, _F32, scale, dev)
-            and _fits(v_scale, _F32, scale, dev))
-
-
-def _pool(k_cache):
-    _device_of(k_cache, "k_cache", _E4M3, 4)
-    return k_cache.shape[0]
-
-
 def _space(workspace, nbytes, dev: int):
     """The caller's workspace, or a new one of nbytes() bytes on device `dev`."""
     if workspace is None:
         return torch.empty(max(nbytes(), 1), dtype=_U8, device=torch.device("cuda", dev))
-    if workspace.dim() != 1 or not _fits(workspace, _U8, workspace.shape, dev):
+    if not (workspace.dtype is _U8 and workspace.dim() == 1 and workspace.get_device() == dev
+            and workspace.is_contiguous()):
         _refuse(dev, (workspace, "workspace", _U8, (None,)))
     return workspace
 
 
 def _check_dev_err(dev_err, dev: int):
-    if dev_err is None:
-        return
-    if dev_err.numel() < 1 or not _fits(dev_err, _I32, dev_err.shape, dev):
-        _dev(dev_err, "dev_err", _I32)
+    _dev(dev_err, "dev_err", _I32)
+    if dev_err.numel() < 1 or dev_err.get_device() != dev:
         raise ValueError(f"dev_err must hold one int32 on cuda:{dev}")
 
 
@@ -697,36 +683,64 @@ def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_
     and raw v quantised to e4m3 under one power-of-two scale per (page, head), rotated idx_k as bf16.  Sequence b's
     new tokens are rows new_start[b] .. new_start[b + 1] - 1 (None: token i belongs to sequence i) and take the
     sequence's last positions.  Returns (q_out, idx_q_out)."""
-    dev = _device_of(q, "q", _BF16, 3)
-    n, H, _ = q.shape
-    P = _pool(k_cache)
-    _device_of(block_table, "block_table", _I32, 2)
-    B, mb = block_table.shape
     if q_out is None:
         q_out = q
     if idx_q_out is None:
         idx_q_out = idx_q
-    heads, idx = (n, H, HEAD_DIM), (n, IDX_DIM)
     try:
-        good = (_fits(q, _BF16, heads, dev) and _fits(idx_q, _BF16, idx, dev) and _fits(k_new, _BF16, heads, dev)
-                and _fits(v_new, _BF16, heads, dev) and _fits(idx_k_new, _BF16, idx, dev)
-                and _fits(tok_pos, _I32, (n,), dev) and _fits(page_pos, _I32, (n,), dev)
-                and _fits(block_table, _I32, (B, mb), dev) and _fits(seq_lens, _I32, (B,), dev)
-                and _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev)
-                and _fits(idx_k_cache, _BF16, (P, BLOCK, IDX_DIM), dev)
-                and (new_start is None or _fits(new_start, _I32, (B + 1,), dev))
-                and (q_out is q or _fits(q_out, _BF16, heads, dev))
-                and (idx_q_out is idx_q or _fits(idx_q_out, _BF16, idx, dev)))
-    except AttributeError:
+        dev = q.get_device()
+        n, H, _ = q.shape
+        P = k_cache.shape[0]
+        B, mb = block_table.shape
+        rows, idx, toks, tile, page = (n, H, HEAD_DIM), (n, IDX_DIM), (n,), (P, H, BLOCK, HEAD_DIM), (P, H)
+        good = (dev >= 0 and q.dtype is _BF16 and q.shape == rows and q.is_contiguous()
+                and idx_q.dtype is _BF16 and idx_q.shape == idx and idx_q.get_device() == dev and idx_q.is_contiguous()
+                and k_new.dtype is _BF16 and k_new.shape == rows and k_new.get_device() == dev and k_new.is_contiguous()
+                and v_new.dtype is _BF16 and v_new.shape == rows and v_new.get_device() == dev and v_new.is_contiguous()
+                and idx_k_new.dtype is _BF16 and idx_k_new.shape == idx and idx_k_new.get_device() == dev
+                and idx_k_new.is_contiguous()
+                and tok_pos.dtype is _I32 and tok_pos.shape == toks and tok_pos.get_device() == dev
+                and tok_pos.is_contiguous()
+                and page_pos.dtype is _I32 and page_pos.shape == toks and page_pos.get_device() == dev
+                and page_pos.is_contiguous()
+                and block_table.dtype is _I32 and block_table.get_device() == dev and block_table.is_contiguous()
+                and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev
+                and seq_lens.is_contiguous()
+                and k_cache.dtype is _E4M3 and k_cache.shape == tile and k_cache.get_device() == dev
+                and k_cache.is_contiguous()
+                and v_cache.dtype is _E4M3 and v_cache.shape == tile and v_cache.get_device() == dev
+                and v_cache.is_contiguous()
+                and k_scale.dtype is _F32 and k_scale.shape == page and k_scale.get_device() == dev
+                and k_scale.is_contiguous()
+                and v_scale.dtype is _F32 and v_scale.shape == page and v_scale.get_device() == dev
+                and v_scale.is_contiguous()
+                and idx_k_cache.dtype is _BF16 and idx_k_cache.shape == (P, BLOCK, IDX_DIM)
+                and idx_k_cache.get_device() == dev and idx_k_cache.is_contiguous()
+                and (new_start is None or (new_start.dtype is _I32 and new_start.shape == (B + 1,)
+                                           and new_start.get_device() == dev and new_start.is_contiguous()))
+                and (q_out is q or (q_out.dtype is _BF16 and q_out.shape == rows and q_out.get_device() == dev
+                                    and q_out.is_contiguous()))
+                and (idx_q_out is idx_q or (idx_q_out.dtype is _BF16 and idx_q_out.shape == idx
+                                            and idx_q_out.get_device() == dev and idx_q_out.is_contiguous())))
+    except _WRONG:
         good = False
     if not good:
-        _refuse(dev, (q, "q", _BF16, heads), (idx_q, "idx_q", _BF16, idx), (k_new, "k_new", _BF16, heads),
-                (v_new, "v_new", _BF16, heads), (idx_k_new, "idx_k_new", _BF16, idx), (tok_pos, "tok_pos", _I32, (n,)),
-                (page_pos, "page_pos", _I32, (n,)), (block_table, "block_table", _I32, (B, mb)),
-                (seq_lens, "seq_lens", _I32, (B,)), *_kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H),
-                (idx_k_cache, "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)), (new_start, "new_start", _I32, (B + 1,)),
-                (q_out, "q_out", _BF16, heads), (idx_q_out, "idx_q_out", _BF16, idx))
-    _check_dev_err(dev_err, dev)
+        _dev(q, "q", _BF16, 3)
+        _dev(k_cache, "k_cache", _E4M3, 4)
+        _dev(block_table, "block_table", _I32, 2)
+        dev, (n, H, _), P, (B, mb) = q.get_device(), q.shape, k_cache.shape[0], block_table.shape
+        rows, idx = (n, H, HEAD_DIM), (n, IDX_DIM)
+        _refuse(dev, (q, "q", _BF16, rows), (_need(idx_q, "idx_q"), "idx_q", _BF16, idx),
+                (_need(k_new, "k_new"), "k_new", _BF16, rows), (_need(v_new, "v_new"), "v_new", _BF16, rows),
+                (_need(idx_k_new, "idx_k_new"), "idx_k_new", _BF16, idx),
+                (_need(tok_pos, "tok_pos"), "tok_pos", _I32, (n,)), (_need(page_pos, "page_pos"), "page_pos", _I32, (n,)),
+                (block_table, "block_table", _I32, (B, mb)), (_need(seq_lens, "seq_lens"), "seq_lens", _I32, (B,)),
+                *_kv8_specs(k_cache, _need(v_cache, "v_cache"), _need(k_scale, "k_scale"), _need(v_scale, "v_scale"), P, H),
+                (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)),
+                (new_start, "new_start", _I32, (B + 1,)), (q_out, "q_out", _BF16, rows),
+                (idx_q_out, "idx_q_out", _BF16, idx))
+    if dev_err is not None:
+        _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_rope_append_kv8, "rope_append_kv8", dev, stream, q.data_ptr(), idx_q.data_ptr(),
             k_new.data_ptr(), v_new.data_ptr(), idx_k_new.data_ptr(), tok_pos.data_ptr(), page_pos.data_ptr(),
             _at(new_start), block_table.data_ptr(), seq_lens.data_ptr(), n, B, H, mb, P, q_out.data_ptr(),
@@ -735,43 +749,70 @@ def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_
     return q_out, idx_q_out
 
 
-def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_seq, out, mass, more=()):
-    """The checks that the attention entry points share; `more`: their other (tensor, name, dtype, shape), which may
-    be None.  n_seq: what the table's first extent must be (None: any).  Returns (device, n, H, P, B, max_blocks, out)."""
-    dev = _device_of(q, "q", _BF16, 3)
-    n, H, _ = q.shape
-    P = _pool(k_cache)
-    _device_of(block_table, "block_table", _I32, 2)
-    B, mb = block_table.shape
-    rows = (n, H, HEAD_DIM)
-    if out is None:
+def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, per_seq, out, mass, dev_err):
+    """The checks that the attention entry points share; per_seq: q has a row per sequence.  Returns (device, n, H, P,
+    B, max_blocks, out)."""
+    if out is None and isinstance(q, torch.Tensor):
         out = torch.empty_like(q)
     try:
-        good = (q.shape[2] == HEAD_DIM and (n_seq is None or n_seq == B) and block_table.get_device() == dev
-                and _fits(seq_lens, _I32, (B,), dev) and _kv8_fit(k_cache, v_cache, k_scale, v_scale, P, H, dev)
-                and _fits(out, _BF16, rows, dev) and (mass is None or _fits(mass, _F32, (B, H, mb), dev)))
-        for t, _, dtype, shape in more:
-            good = good and (t is None or _fits(t, dtype, shape, dev))
-    except AttributeError:
+        dev = q.get_device()
+        n, H, _ = q.shape
+        P = k_cache.shape[0]
+        B, mb = block_table.shape
+        rows, tile, page = (n, H, HEAD_DIM), (P, H, BLOCK, HEAD_DIM), (P, H)
+        good = (dev >= 0 and q.dtype is _BF16 and q.shape == rows and q.is_contiguous()
+                and k_cache.dtype is _E4M3 and k_cache.shape == tile and k_cache.get_device() == dev
+                and k_cache.is_contiguous()
+                and v_cache.dtype is _E4M3 and v_cache.shape == tile and v_cache.get_device() == dev
+                and v_cache.is_contiguous()
+                and k_scale.dtype is _F32 and k_scale.shape == page and k_scale.get_device() == dev
+                and k_scale.is_contiguous()
+                and v_scale.dtype is _F32 and v_scale.shape == page and v_scale.get_device() == dev
+                and v_scale.is_contiguous()
+                and block_table.dtype is _I32 and block_table.get_device() == dev and block_table.is_contiguous()
+                and seq_lens.dtype is _I32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev
+                and seq_lens.is_contiguous()
+                and out.dtype is _BF16 and out.shape == rows and out.get_device() == dev and out.is_contiguous()
+                and (not per_seq or n == B)
+                and (mass is None or (mass.dtype is _F32 and mass.shape == (B, H, mb) and mass.get_device() == dev
+                                      and mass.is_contiguous())))
+    except _WRONG:
         good = False
     if not good:
-        _refuse(dev, (q, "q", _BF16, rows), (block_table, "block_table", _I32, (B if n_seq is None else n_seq, mb)),
-                (seq_lens, "seq_lens", _I32, (B,)), *_kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H),
-                (out, "out", _BF16, rows), (mass, "mass", _F32, (B, H, mb)), *more)
+        _dev(q, "q", _BF16, 3)
+        _dev(k_cache, "k_cache", _E4M3, 4)
+        _dev(block_table, "block_table", _I32, 2)
+        dev, (n, H, _), P, (B, mb) = q.get_device(), q.shape, k_cache.shape[0], block_table.shape
+        _refuse(dev, (q, "q", _BF16, (n, H, HEAD_DIM)), (block_table, "block_table", _I32, (n if per_seq else B, mb)),
+                (_need(seq_lens, "seq_lens"), "seq_lens", _I32, (B,)),
+                *_kv8_specs(k_cache, _need(v_cache, "v_cache"), _need(k_scale, "k_scale"), _need(v_scale, "v_scale"), P, H),
+                (out, "out", _BF16, (n, H, HEAD_DIM)), (mass, "mass", _F32, (B, H, mb)))
+    if dev_err is not None:
+        _check_dev_err(dev_err, dev)
     return dev, n, H, P, B, mb, out
+
+
+def _index_args(dev, idx_q, idx_k_cache, sel, n, P):
+    """The indexer's tensors of a whole step, and the selection's output."""
+    if sel is None:
+        sel = torch.empty((n, N_SEL), dtype=_I32, device=torch.device("cuda", dev))
+    _refuse(dev, (_need(idx_q, "idx_q"), "idx_q", _BF16, (n, IDX_DIM)),
+            (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)), (sel, "sel", _I32, (n, N_SEL)))
+    return sel
 
 
 def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, sel, q_seq=None, q_pos=None, *,
                     scale: float | None = None, out=None, mass=None, dev_err=None, stream=None) -> torch.Tensor:
     """sparse_attn over the 8-bit cache: bf16 [n_q, H, 128].  mass [B, H, max_blocks] fp32 (one query per
     sequence, q_seq None): each selected block's attention weight is added to its total."""
-    n_q = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    dev, n_q, H, P, B, mb, out = _attn_args(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
-        ((_need(sel, "sel"), "sel", _I32, (n_q, N_SEL)), (q_seq, "q_seq", _I32, (n_q,)), (q_pos, "q_pos", _I32, (n_q,))))
+    dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
+                                            mass, dev_err)
+    _need(sel, "sel")
+    if not (sel.dtype is _I32 and sel.shape == (n_q, N_SEL) and sel.get_device() == dev and sel.is_contiguous()
+            and q_seq is None and q_pos is None):
+        _refuse(dev, (sel, "sel", _I32, (n_q, N_SEL)), (q_seq, "q_seq", _I32, (n_q,)), (q_pos, "q_pos", _I32, (n_q,)))
     if mass is not None and q_seq is not None:
         raise ValueError("mass needs one query per sequence: q_seq must be None")
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_sparse_attn_kv8, "sparse_attn_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             _at(q_seq), _at(q_pos), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
@@ -779,28 +820,13 @@ def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     return out
 
 
-_SCALE = HEAD_DIM ** -0.5
-
-
-def _need(t, name: str):
-    if t is None:
-        raise TypeError(f"{name} must be a torch.Tensor")
-    return t
-
-
 def sparse_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, *, out=None,
                       sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_decode over the 8-bit cache.  Returns (out [B,H,128] bf16, sel [B,16] int32)."""
-    dev = _device_of(q, "q", _BF16, 3)
-    B, P = q.shape[0], _pool(k_cache)
-    if sel is None:
-        sel = torch.empty((B, N_SEL), dtype=_I32, device=q.device)
-    dev, B, H, P, _, mb, out = _attn_args(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, B, out, mass,
-        ((sel, "sel", _I32, (B, N_SEL)), (_need(idx_q, "idx_q"), "idx_q", _BF16, (B, IDX_DIM)),
-         (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM))))
+    dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, True, out,
+                                          mass, dev_err)
+    sel = _index_args(dev, idx_q, idx_k_cache, sel, B, P)
     workspace = _space(workspace, lambda: workspace_bytes(B, H, mb), dev)
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_sparse_decode_kv8, "sparse_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), B, H, mb, P, out.data_ptr(), sel.data_ptr(), _at(mass),
@@ -813,10 +839,9 @@ def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     """dense_decode over the 8-bit cache: blocks [0, ref_blocks) plus the 4-block local window, or all of them
     when ref_blocks is None.  Returns out [B,H,128] bf16; mass [B, H, max_blocks] receives every attended block's
     weight."""
-    n_seq = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, n_seq, out, mass)
+    dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, True, out,
+                                          mass, dev_err)
     workspace = _space(workspace, lambda: dense_kv8_workspace_bytes(B, H, mb), dev)
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_dense_decode_kv8, "dense_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             mb if ref_blocks is None else int(ref_blocks), B, H, mb, P, out.data_ptr(), _at(mass),
@@ -829,12 +854,10 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                         stream=None) -> torch.Tensor:
     """sparse_attn_seq over the 8-bit cache: many queries of sequence `seq` over the given selection.  Returns out
     [n_q,H,128] bf16; row `seq` of mass [B, H, max_blocks] receives the queries' weights."""
-    n_q = q.shape[0] if isinstance(q, torch.Tensor) and q.dim() else 0
-    dev, n_q, H, P, B, mb, out = _attn_args(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
-        ((_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)), (_need(sel, "sel"), "sel", _I32, (n_q, N_SEL))))
+    dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
+                                            mass, dev_err)
+    _refuse(dev, (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)), (_need(sel, "sel"), "sel", _I32, (n_q, N_SEL)))
     workspace = _space(workspace, lambda: sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), dev)
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_sparse_attn_seq_kv8, "sparse_attn_seq_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             int(seq), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
@@ -845,17 +868,11 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
 def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache, block_table, seq_lens, seq: int,
                        q_pos, *, out=None, sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_prefill over the 8-bit cache.  Returns (out [n_q,H,128] bf16, sel [n_q,16] int32)."""
-    dev = _device_of(q, "q", _BF16, 3)
-    n_q, P = q.shape[0], _pool(k_cache)
-    if sel is None:
-        sel = torch.empty((n_q, N_SEL), dtype=_I32, device=q.device)
-    dev, n_q, H, P, B, mb, out = _attn_args(
-        q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, None, out, mass,
-        ((sel, "sel", _I32, (n_q, N_SEL)), (_need(idx_q, "idx_q"), "idx_q", _BF16, (n_q, IDX_DIM)),
-         (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)),
-         (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,))))
+    dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
+                                            mass, dev_err)
+    sel = _index_args(dev, idx_q, idx_k_cache, sel, n_q, P)
+    _refuse(dev, (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)))
     workspace = _space(workspace, lambda: prefill_kv8_workspace_bytes(n_q, H, mb), dev)
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_sparse_prefill_kv8, "sparse_prefill_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), int(seq), q_pos.data_ptr(), n_q, B, H, mb, P, out.data_ptr(),
@@ -869,27 +886,41 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
     and those of the others with the highest totals over the heads (lower id on ties) stay.  Returns (new_mass
     [B,H,max_blocks] fp32, new_table [B,max_blocks] int32, new_lens [B] int32, freed [B,max_blocks] int32 pages,
     n_freed [B] int32); the first three may be the inputs themselves."""
-    dev = _device_of(mass, "mass", _F32, 3)
-    B, H, mb = mass.shape
-    new_mass = torch.empty_like(mass) if new_mass is None else new_mass
-    new_table = torch.empty_like(block_table) if new_table is None else new_table
-    new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
-    freed = torch.empty_like(block_table) if freed is None else freed
-    n_freed = torch.empty_like(seq_lens) if n_freed is None else n_freed
-    table, lens = (B, mb), (B,)
     try:
-        good = (_fits(block_table, _I32, table, dev) and _fits(seq_lens, _I32, lens, dev)
-                and _fits(new_mass, _F32, mass.shape, dev) and _fits(new_table, _I32, table, dev)
-                and _fits(new_lens, _I32, lens, dev) and _fits(freed, _I32, table, dev)
-                and _fits(n_freed, _I32, lens, dev))
-    except AttributeError:
+        new_mass = torch.empty_like(mass) if new_mass is None else new_mass
+        new_table = torch.empty_like(block_table) if new_table is None else new_table
+        new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
+        freed = torch.empty_like(block_table) if freed is None else freed
+        n_freed = torch.empty_like(seq_lens) if n_freed is None else n_freed
+        dev = mass.get_device()
+        B, H, mb = totals = mass.shape
+        table, lens = (B, mb), (B,)
+        good = (dev >= 0 and mass.dtype is _F32 and mass.is_contiguous()
+                and block_table.dtype is _I32 and block_table.shape == table and block_table.get_device() == dev
+                and block_table.is_contiguous()
+                and seq_lens.dtype is _I32 and seq_lens.shape == lens and seq_lens.get_device() == dev
+                and seq_lens.is_contiguous()
+                and new_mass.dtype is _F32 and new_mass.shape == totals and new_mass.get_device() == dev
+                and new_mass.is_contiguous()
+                and new_table.dtype is _I32 and new_table.shape == table and new_table.get_device() == dev
+                and new_table.is_contiguous()
+                and new_lens.dtype is _I32 and new_lens.shape == lens and new_lens.get_device() == dev
+                and new_lens.is_contiguous()
+                and freed.dtype is _I32 and freed.shape == table and freed.get_device() == dev and freed.is_contiguous()
+                and n_freed.dtype is _I32 and n_freed.shape == lens and n_freed.get_device() == dev
+                and n_freed.is_contiguous())
+    except _WRONG:
         good = False
     if not good:
-        _refuse(dev, (block_table, "block_table", _I32, table), (seq_lens, "seq_lens", _I32, lens),
-                (new_mass, "new_mass", _F32, (B, H, mb)), (new_table, "new_table", _I32, table),
-                (new_lens, "new_lens", _I32, lens), (freed, "freed", _I32, table), (n_freed, "n_freed", _I32, lens))
+        _dev(mass, "mass", _F32, 3)
+        dev, (B, H, mb) = mass.get_device(), mass.shape
+        _refuse(dev, (_need(block_table, "block_table"), "block_table", _I32, (B, mb)),
+                (_need(seq_lens, "seq_lens"), "seq_lens", _I32, (B,)), (new_mass, "new_mass", _F32, (B, H, mb)),
+                (new_table, "new_table", _I32, (B, mb)), (new_lens, "new_lens", _I32, (B,)),
+                (freed, "freed", _I32, (B, mb)), (n_freed, "n_freed", _I32, (B,)))
+    if dev_err is not None:
+        _check_dev_err(dev_err, dev)
     workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev)
-    _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_evict_blocks, "evict_blocks", dev, stream, mass.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), B, H, mb, int(keep_blocks), int(n_sink), new_mass.data_ptr(), new_table.data_ptr(),
             new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), workspace.data_ptr(), workspace.numel(),
