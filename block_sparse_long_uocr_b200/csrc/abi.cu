@@ -576,6 +576,8 @@ inline uocr_status_t check_seq_kv8(const void *q, const void *k_cache, const voi
         return UOCR_ERR_INVALID_ARG;
     if ((st = check_kv8(k_cache, v_cache, k_scale, v_scale, H)) != UOCR_OK) return st;
     if ((long long)n_q * UOCR_N_SEL > 0x7fffffffLL || (long long)n_q * H > 0x7fffffffLL / 2) return UOCR_ERR_UNSUPPORTED;
+    // a block's sum over the queries is kept in 64 bits with 40 behind the point
+    if (mass && n_q > (1 << 23)) return UOCR_ERR_UNSUPPORTED;
     // units of work and block totals are counted in int32
     if ((long long)uocr::prefill_item_bound(n_q, max_blocks) * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;
     if ((long long)max_blocks * H > 0x3fffffffLL) return UOCR_ERR_UNSUPPORTED;

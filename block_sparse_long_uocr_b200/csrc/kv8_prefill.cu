@@ -290,7 +290,9 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                 for (int e = 0; e < 4; ++e) s[nt][e] = -s[nt][e];
             ks = -ks;
         }
-        const float fa = ua * ks, fb = ub * ks;
+        // (a factor past fp32's range stays finite, so that a score of 0 stays 0)
+        const float fa = fabsf(ua * ks) > 3.4028235e38f ? 3.4028235e38f : ua * ks;
+        const float fb = fabsf(ub * ks) > 3.4028235e38f ? 3.4028235e38f : ub * ks;
         const bool partly = near < kBlock;   // some query does not see the whole block
         auto hidden = [&](int nt, int e, int pos) { return t0 + 8 * nt + 4 * e + c > pos; };
         if (partly) {

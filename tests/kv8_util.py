@@ -96,7 +96,7 @@ def attend(q, k, v, ks, vs, pages, blocks, p, scale):
     out = torch.einsum("ht,htd->hd", w, vv)
     full = torch.zeros((H, n * BLOCK), dtype=torch.float64)
     full[:, see] = w
-    mag = (torch.einsum("htd,hd->ht", kk.abs(), qd.abs()) * scale).amax(dim=1)
+    mag = (torch.einsum("htd,hd->ht", kk.abs(), qd.abs()) * abs(scale)).amax(dim=1)   # magnitudes: of the scale too
     return out, full.reshape(H, n, BLOCK).sum(-1), mag, vv.abs().amax(dim=(1, 2))
 
 

@@ -171,6 +171,80 @@ def test_sparse_device_errors(uocr, cuda_device):
     check_rows(c, out, mass, [(1, 1, 299, left), (2, 2, 99, sel[2].tolist())])
 
 
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-3])
+def test_any_finite_scale(uocr, cuda_device, scale):
+    """A negative scale turns the order of the scores round, 0 makes them all equal (also next to tokens that are
+    behind the query)."""
+    n, total = 20, 150
+    c = Case([total], 3, seed=17, n_q=n)
+    pos = list(range(total - n, total))
+    sel = torch.full((n, 16), -1, dtype=torch.int32)
+    sel[:, 3:8] = torch.arange(5)
+    sel[:14, 7] = torch.tensor([4 if p >= 128 else -1 for p in pos[:14]], dtype=torch.int32)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    qp, se = torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device)
+    rows = [(i, 0, pos[i], sel[i].tolist()) for i in range(n)]
+    one = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, se, torch.zeros(n, dtype=torch.int32, device=cuda_device), qp, scale=scale)
+    check_rows(c, one, None, rows, scale=scale)
+    mass = c.mass.to(cuda_device)
+    many = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, qp, se, scale=scale, mass=mass)
+    check_rows(c, many, mass, rows, scale=scale, many=True)
+
+
+@pytest.mark.parametrize("H", [64])
+def test_most_heads(uocr, cuda_device, H):
+    c = Case([70, 700], H, seed=18)
+    sel = c.select([69, 699])
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    rows = [(i, i, c.lens[i] - 1, sel[i].tolist()) for i in range(2)]
+    mass = c.mass.to(cuda_device)
+    check_rows(c, uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass), mass, rows)
+    out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl)
+    check_rows(c, out, None, [(i, i, c.lens[i] - 1, list(range(-(-c.lens[i] // 32)))) for i in range(2)])
+    out = uocr.sparse_attn_seq_kv8(q[1:], k, v, ks, vs, bt, sl, 1, torch.tensor([699], dtype=torch.int32, device=cuda_device),
+                                   sel[1:].to(cuda_device))
+    c.q = c.q[1:]
+    check_rows(c, out, None, [(0, 1, 699, sel[1].tolist())], many=True)
+
+
+def test_pools_past_32_bit_offsets(uocr, cuda_device):
+    """Pages whose tiles lie behind 4 GiB: read by every form, written by the append."""
+    H, P, total = 10, 110000, 300
+    c = Case([total], H, seed=19)
+    used = c.table[0, :10].long()
+    far = torch.arange(P - 10, P)
+    codes = [torch.zeros(P * H * 4096, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    scales = [torch.ones((P, H), device=cuda_device) for _ in range(2)]
+    k8, v8 = [x.view(torch.float8_e4m3fn).view(P, H, 32, 128) for x in codes]
+    for dst, src in ((codes[0], c.k), (codes[1], c.v)):
+        dst.view(P, H, 32, 128)[P - 10:] = src.view(torch.uint8)[used].to(cuda_device)
+    scales[0][P - 10:], scales[1][P - 10:] = c.ks[used].to(cuda_device), c.vs[used].to(cuda_device)
+    bt = far.to(torch.int32)[None].to(cuda_device).contiguous()
+    q, sl = c.q.to(cuda_device), c.sl.to(cuda_device)
+    sel = torch.full((1, 16), -1, dtype=torch.int32)
+    sel[0, :10] = torch.arange(10)
+    pos = torch.tensor([total - 1], dtype=torch.int32, device=cuda_device)
+    rows = [(0, 0, total - 1, list(range(10)))]
+    check_rows(c, uocr.sparse_attn_kv8(q, k8, v8, *scales, bt, sl, sel.to(cuda_device)), None, rows)
+    check_rows(c, uocr.dense_decode_kv8(q, k8, v8, *scales, bt, sl), None, rows)
+    check_rows(c, uocr.sparse_attn_seq_kv8(q, k8, v8, *scales, bt, sl, 0, pos, sel.to(cuda_device)), None, rows, many=True)
+    g = torch.Generator().manual_seed(1)
+    for n in (1, 40):    # both of the append's forms
+        rnd = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16)  # noqa: E731
+        s = {"q": rnd(n, H, 128), "idx_q": rnd(n, 128), "k_new": rnd(n, H, 128), "v_new": rnd(n, H, 128), "idx_k_new": rnd(n, 128),
+             "tok": torch.arange(n, dtype=torch.int32), "page": torch.zeros(n, dtype=torch.int32), "idx_k": torch.zeros((10, 32, 128), dtype=torch.bfloat16)}
+        for name, x, sc in (("k", k8, scales[0]), ("v", v8, scales[1])):
+            s[name], s[name + "_scale"] = x[P - 10:].cpu(), sc[P - 10:].cpu()
+        want = ref.append(s, [0, n], [total], torch.arange(10, dtype=torch.int32)[None])
+        ik = torch.zeros((P, 32, 128), dtype=torch.bfloat16, device=cuda_device)
+        d = {x: s[x].to(cuda_device) for x in ("q", "idx_q", "k_new", "v_new", "idx_k_new", "tok", "page")}
+        uocr.rope_append_kv8(*d.values(), bt, sl, k8, v8, *scales, ik, torch.tensor([0, n], dtype=torch.int32, device=cuda_device))
+        for name, x, sc in (("k", k8, scales[0]), ("v", v8, scales[1])):
+            assert same_codes(x[P - 10:].cpu(), want[name])
+            assert np.array_equal(sc[P - 10:].cpu().double().numpy(), want[name + "_scale"])
+            assert (x[:1000].view(torch.uint8) == 0).all() and (sc[:P - 10] == 1).all()
+
+
 @pytest.mark.parametrize("lens,ref_blocks", [([1], None), ([0, 31, 32, 33], None), ([2000, 513, 5000], None), ([2000, 513, 5000, 0, 90], 3),
                                              ([1000, 64], 0), ([700, 3000], 22), ([9001], 10 ** 6)])
 @pytest.mark.parametrize("H", [1, 10])
