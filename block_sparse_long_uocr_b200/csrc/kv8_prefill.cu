@@ -4,9 +4,9 @@
 // The result of sparse_attn_kv8 for every query (Unlimited-OCR-2 walk-through,
 // news.rkmt.cn/news/25027, section 五 step 4), computed block by block as the bf16 form does
 // (prefill_attn.cu), so that a (block, head) tile is read once for all the queries that chose it:
-//   1. prepare   a CTA per query: its selection is checked and counted per block, and its rows are
-//                turned into fp16, in the order in which the products load them, each row times a
-//                power of two that brings its largest element to 2^14 (exact, see kv8.cuh);
+//   1. prepare   the selections are checked and counted per block, and the queries' rows turned into
+//                fp16, in the order in which the products load them, each row times a power of two
+//                that brings its largest element to 2^14 (exact, see kv8.cuh);
 //   2. invert    per block, the list of the (query, slot) entries that chose it, in items of at
 //                most 16 (the bf16 form's kernel);
 //   3. blocks    one warp per (item, head): S = Q K8^T (16 x 32), an fp32 softmax per row,
@@ -96,53 +96,48 @@ __device__ __forceinline__ void discard_line(const void *p) {   // 128 bytes, no
 }  // namespace
 
 // q16 [n_q][H][16] pieces of 8 dims: piece 4 x + c holds dims 64 (x / 2) + 16 c + 8 (x % 2) .. + 7.
-__global__ void __launch_bounds__(128)
+// The first CTAs take 16 (query, head) rows each, 16 lanes a row; the others 16 queries' selections.
+__global__ void __launch_bounds__(256)
 kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel, const int32_t *__restrict__ q_pos,
-                   const int32_t *__restrict__ seq_len_ptr, int H, int max_blocks, int32_t *__restrict__ sel_ws,
-                   int32_t *counts, uint4 *__restrict__ q16, float *__restrict__ unit, int32_t *dev_err) {
-    const int i = blockIdx.x, tid = threadIdx.x;
-    // (No kernel here lets the next one start early: waiting CTAs hold room that the running ones' later
-    // CTAs need; 79 us became 85 to 88 for 2048 queries.)
-    // 16 lanes per (query, head) row, 8 dims each: the rows are inputs of the call, so the first round
-    // is on its way before the wait
-    const int l = tid & 15;
-    uint4 raw = (tid >> 4) < H ? __ldg(q + ((size_t)i * H + (tid >> 4)) * 16 + l) : make_uint4(0u, 0u, 0u, 0u);
-    pdl_wait();
-    if (tid < kSel) {
+                   const int32_t *__restrict__ seq_len_ptr, int n_q, int n_rows, int row_ctas, int max_blocks,
+                   int32_t *__restrict__ sel_ws, int32_t *counts, uint4 *__restrict__ q16,
+                   float *__restrict__ unit, int32_t *dev_err) {
+    const int l = threadIdx.x & 15;
+    if ((int)blockIdx.x >= row_ctas) {
+        const int i = ((int)blockIdx.x - row_ctas) * 16 + (threadIdx.x >> 4);
+        pdl_wait();   // the selection may come from the kernel before, as the zeroed counts do
+        if (i >= n_q) return;
         const int len = __ldg(seq_len_ptr), p = __ldg(q_pos + i);
         const bool ok = p >= 0 && p < len && len <= max_blocks * kBlock;
-        if (!ok && tid == 0) flag_error(dev_err, UOCR_DEVERR_POS);
-        int j = ok ? __ldcg(sel + (size_t)i * kSel + tid) : -1;
+        if (!ok && l == 0) flag_error(dev_err, UOCR_DEVERR_POS);
+        int j = ok ? __ldcg(sel + (size_t)i * kSel + l) : -1;
         if (j > p / kBlock) {
             flag_error(dev_err, UOCR_DEVERR_SEL);
             j = -1;
         }
         if (j < 0) j = -1;
-        sel_ws[(size_t)i * kSel + tid] = j;
+        sel_ws[(size_t)i * kSel + l] = j;
         if (j >= 0) atomicAdd(counts + j, 1);
+        return;
     }
-    for (int h0 = 0; h0 < H; h0 += 8) {
-        const int h = h0 + (tid >> 4);
-        const bool live = h < H;
-        float x[8];
-        float amax = 0.f;
-        bf16x8_to_f32(raw, x);
-        raw = h + 8 < H ? __ldg(q + ((size_t)i * H + h + 8) * 16 + l) : make_uint4(0u, 0u, 0u, 0u);
+    const int row = blockIdx.x * 16 + (threadIdx.x >> 4);
+    const bool live = row < n_rows;
+    float x[8];
+    float amax = 0.f;
+    bf16x8_to_f32(live ? __ldg(q + (size_t)row * 16 + l) : make_uint4(0u, 0u, 0u, 0u), x);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
 #pragma unroll
-        for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float inv;
-        const float s = f16_row_scale(amax, inv);
-        if (live) {
-            // dims 8 l ..: half l / 8, c = (l % 8) / 2, x % 2 = l % 2
-            const int piece = 4 * (2 * (l >> 3) + (l & 1)) + ((l & 7) >> 1);
-            q16[((size_t)i * H + h) * 16 + piece] =
-                make_uint4(pack_f16(x[0] * s, x[1] * s), pack_f16(x[2] * s, x[3] * s), pack_f16(x[4] * s, x[5] * s),
-                           pack_f16(x[6] * s, x[7] * s));
-            if (l == 0) unit[(size_t)i * H + h] = inv;
-        }
-    }
+    for (int o = 1; o < 16; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    float inv;
+    const float s = f16_row_scale(amax, inv);
+    pdl_wait();   // the workspace may still be read by the call before
+    if (!live) return;
+    // dims 8 l ..: half l / 8, c = (l % 8) / 2, x % 2 = l % 2
+    const int piece = 4 * (2 * (l >> 3) + (l & 1)) + ((l & 7) >> 1);
+    q16[(size_t)row * 16 + piece] = make_uint4(pack_f16(x[0] * s, x[1] * s), pack_f16(x[2] * s, x[3] * s),
+                                               pack_f16(x[4] * s, x[5] * s), pack_f16(x[6] * s, x[7] * s));
+    if (l == 0) unit[row] = inv;
 }
 
 __global__ void __launch_bounds__(kBlkWarps * 32, kBlkCtas)
@@ -607,10 +602,11 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     cfg.stream = c.stream;
     cfg.attrs = attr;
     cfg.numAttrs = c.pdl ? 1 : 0;
-    cfg.gridDim = dim3((unsigned)n_q);
-    cfg.blockDim = dim3(128);
-    cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prepare_kernel, (const uint4 *)q, sel, q_pos, seq_len_ptr, H,
-                                       max_blocks, sel_ws, counts, q16, unit, dev_err);
+    const int n_rows = n_q * H, row_ctas = (n_rows + 15) / 16;   // below 2^30 rows
+    cfg.gridDim = dim3((unsigned)(row_ctas + (n_q + 15) / 16));
+    cfg.blockDim = dim3(256);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kv8_prepare_kernel, (const uint4 *)q, sel, q_pos, seq_len_ptr, n_q, n_rows,
+                                       row_ctas, max_blocks, sel_ws, counts, q16, unit, dev_err);
     if (e != cudaSuccess) return e;
     e = launch_prefill_invert(c, counts, bt_row, sel_ws, q_pos, n_q, max_blocks, (int32_t *)(base + w.fill_off), items,
                               n_items, list);
@@ -631,11 +627,10 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = 0;
 
-    const long long rows = (long long)n_q * H;
-    cfg.gridDim = dim3((unsigned)((rows + 2 * kMrgWarps - 1) / (2 * kMrgWarps)));
+    cfg.gridDim = dim3((unsigned)((n_rows + 2 * kMrgWarps - 1) / (2 * kMrgWarps)));
     cfg.blockDim = dim3(kMrgWarps * 32);
     e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, (const int32_t *)sel_ws, (const uint4 *)part_o, (const float4 *)ml,
-                           (int)rows, H, max_blocks, (uint4 *)out, mass_fx);
+                           n_rows, H, max_blocks, (uint4 *)out, mass_fx);
     if (e != cudaSuccess || !mass_row) return e;
     const int n = H * max_blocks;
     cfg.gridDim = dim3((unsigned)((n + 255) / 256));
