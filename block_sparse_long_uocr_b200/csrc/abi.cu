@@ -604,13 +604,11 @@ uocr_status_t uocr_sparse_attn_seq_kv8(const void *q, const void *k_cache, const
         return UOCR_ERR_WORKSPACE;
     uocr::LaunchCtx c;
     if ((st = make_ctx(stream, false, c)) != UOCR_OK) return st;
-    cudaError_t e = uocr::zero_prefill_kv8(c, workspace, n_q, H, max_blocks, nullptr);
+    cudaError_t e = uocr::zero_prefill_kv8(c, workspace, n_q, H, max_blocks, mass != nullptr, nullptr);
     if (e != cudaSuccess) return cuda_status(e);
     const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
-    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, block_table + (size_t)seq * max_blocks, seq_lens + seq,
-                                                q_pos, sel, n_q, H, max_blocks, num_pages, scale, out,
-                                                mass ? mass + (size_t)seq * H * max_blocks : nullptr, workspace,
-                                                dev_err));
+    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, block_table, seq_lens, seq, q_pos, sel, n_q, B, H, max_blocks,
+                                                num_pages, scale, out, mass, workspace, dev_err));
 }
 
 uocr_status_t uocr_sparse_prefill_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
@@ -632,7 +630,7 @@ uocr_status_t uocr_sparse_prefill_kv8(const void *q, const void *k_cache, const 
     float *scores = (float *)((char *)workspace + w.scores_off);
     char *attn_ws = (char *)workspace + w.total;
     int32_t *sched = nullptr;
-    cudaError_t e = uocr::zero_prefill_kv8(c, attn_ws, n_q, H, max_blocks, &sched);
+    cudaError_t e = uocr::zero_prefill_kv8(c, attn_ws, n_q, H, max_blocks, mass != nullptr, &sched);
     if (e != cudaSuccess) return cuda_status(e);
     const int32_t *bt_row = block_table + (size_t)seq * max_blocks;
     e = uocr::launch_prefill_index_gemm(c, idx_q, idx_k_cache, bt_row, seq_lens + seq, q_pos, n_q, max_blocks,
@@ -643,10 +641,8 @@ uocr_status_t uocr_sparse_prefill_kv8(const void *q, const void *k_cache, const 
     if (e != cudaSuccess) return cuda_status(e);
     const float scale = 1.0f / sqrtf((float)UOCR_HEAD_DIM);
     const uocr::Kv8Cache kv{k_cache, v_cache, k_scale, v_scale};
-    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, bt_row, seq_lens + seq, q_pos, sel_out, n_q, H, max_blocks,
-                                                num_pages, scale, out,
-                                                mass ? mass + (size_t)seq * H * max_blocks : nullptr, attn_ws,
-                                                dev_err));
+    return cuda_status(uocr::launch_prefill_kv8(c, q, kv, block_table, seq_lens, seq, q_pos, sel_out, n_q, B, H,
+                                                max_blocks, num_pages, scale, out, mass, attn_ws, dev_err));
 }
 
 size_t uocr_evict_workspace_bytes(int B, int H, int max_blocks) {

@@ -134,23 +134,28 @@ cudaError_t launch_rope_append_kv8(const LaunchCtx &c, const void *q, const void
                                    const int32_t *seq_lens, int n, int B, int H, int max_blocks, int num_pages,
                                    void *q_out, void *idx_q_out, void *k_cache, void *v_cache, float *k_scale,
                                    float *v_scale, void *idx_k_cache, int32_t *dev_err);
-// mass [B][H][max_blocks] or NULL (q_seq NULL then: one query per sequence).
+// mass [B][H][max_blocks] or NULL (q_seq NULL then: one query per sequence).  fixed_seq >= 0: every
+// query belongs to that sequence, at q_pos, and mass_fx [H][max_blocks] (or NULL) receives the
+// weights as integers (see kv8.cuh).
 cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
                                    const int32_t *seq_lens, const int32_t *q_seq, const int32_t *q_pos,
                                    const int32_t *sel, int n_q, int B, int H, int max_blocks, int num_pages,
-                                   float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err);
+                                   float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err,
+                                   int fixed_seq = -1, unsigned long long *mass_fx = nullptr);
 size_t dense_kv8_workspace(int n_q, int H, int max_blocks);
 cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
                              const int32_t *seq_lens, int B, int H, int max_blocks, int num_pages, int ref_blocks,
                              float scale, void *out, float *mass, void *ws, int32_t *dev_err);
 size_t prefill_kv8_workspace(int n_q, int H, int max_blocks);
-// Zeroes what launch_prefill_kv8 needs zero; *sched: the scoring GEMM's zeroed work-unit counter.
-cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, int32_t **sched);
-// mass_row [H][max_blocks] of the sequence, or NULL.
-cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt_row,
-                               const int32_t *seq_len_ptr, const int32_t *q_pos, const int32_t *sel, int n_q, int H,
-                               int max_blocks, int num_pages, float scale, void *out, float *mass_row, void *ws,
-                               int32_t *dev_err);
+// Zeroes what launch_prefill_kv8 needs zero (totals: it is given a mass); *sched, unless NULL: the
+// scoring GEMM's zeroed work-unit counter.
+cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, bool totals,
+                             int32_t **sched);
+// Queries of sequence seq.  c.pdl: sel comes from the selection kernel just launched.
+cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
+                               const int32_t *seq_lens, int seq, const int32_t *q_pos, const int32_t *sel, int n_q,
+                               int B, int H, int max_blocks, int num_pages, float scale, void *out, float *mass,
+                               void *ws, int32_t *dev_err);
 
 // Eviction of blocks by accumulated attention weight.
 size_t evict_workspace(int B, int max_blocks);

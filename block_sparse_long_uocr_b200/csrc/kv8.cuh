@@ -225,5 +225,10 @@ __device__ __forceinline__ void weighted_sum8(float (&acc)[16], const float (&p)
 // The weight a block received, as it is added to the running totals: a weight that is not finite
 // (a query with infinities or NaN) adds nothing, so that one bad query does not spoil them.
 __device__ __forceinline__ float finite_weight(float w) { return w >= 0.f && w <= 3.4e38f ? w : 0.f; }
+// The same as a multiple of 2^-40, for sums whose order is not fixed.
+constexpr float kMassUnit = 1.f / (1ll << 40);
+__device__ __forceinline__ unsigned long long fixed_weight(float w) {
+    return __float2ull_rn(finite_weight(w) / kMassUnit);
+}
 
 }  // namespace uocr

@@ -158,8 +158,8 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
                        const int32_t *__restrict__ bt, const int32_t *__restrict__ seq_lens,
                        const int32_t *__restrict__ q_seq, const int32_t *__restrict__ q_pos,
                        const int32_t *__restrict__ sel, int B, int H, int max_blocks, int num_pages,
-                       float scale_log2, int implicit_local, __nv_bfloat16 *__restrict__ out,
-                       float *__restrict__ mass, int32_t *dev_err) {
+                       float scale_log2, int implicit_local, int fixed_seq, __nv_bfloat16 *__restrict__ out,
+                       float *__restrict__ mass, unsigned long long *mass_fx, int32_t *dev_err) {
     constexpr int kStep = kSWarps * kCluster, kPer = kSel / kStep;
     __shared__ __align__(16) Merge8<kSWarps> s;
     __shared__ __align__(16) Merge8<kCluster> s_all;   // of CTA 0: the CTAs' states
@@ -176,8 +176,12 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     int j = implicit_local ? -2 : ld_pinned(my_sel);
     const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
-    const bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err,
-                                  threadIdx.x == 0 && h == 0 && rank == 0, r);
+    const bool report = threadIdx.x == 0 && h == 0 && rank == 0;
+    bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err, report, r, fixed_seq);
+    if (fixed_seq >= 0 && ok && r.p < 0) {   // a chunk's positions are the caller's
+        if (report) flag_error(dev_err, UOCR_DEVERR_POS);
+        ok = false;
+    }
     if (!ok) j = -1;
     if (j == -2) {   // after the selection kernel: slots that do not depend on the scores (see sparse_attn.cu)
         if (r.nb <= kSel)
@@ -234,7 +238,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     if (rank == 0) {
         // L is 0 for a query without a visible token, NaN where a score is
         out[(size_t)ih * kD + d] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
-        if (totals && warp == 0) {
+        if ((totals || mass_fx) && warp == 0) {
             // one writer per block: the first slot that names it adds the weights of all that do
             const int x = lane & 15;
             const int block = __float_as_int(s_slot[2][x]);
@@ -248,8 +252,12 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
                 }
                 w = all;
             }
-            if (lane < kSel && block >= 0 && lane == __ffs(same) - 1 && L > 0.f)
-                totals[block] = s_slot[3][x] + finite_weight(w / L);
+            if (lane < kSel && block >= 0 && lane == __ffs(same) - 1 && L > 0.f) {
+                if (totals)
+                    totals[block] = s_slot[3][x] + finite_weight(w / L);
+                else   // many queries of one sequence: a sum of integers, in any order
+                    atomicAdd(mass_fx + (size_t)h * max_blocks + block, fixed_weight(w / L));
+            }
         }
     }
     // warps whose blocks were known in advance did not wait for the selection kernel: this grid
@@ -376,7 +384,8 @@ dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int m
 cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
                                    const int32_t *seq_lens, const int32_t *q_seq, const int32_t *q_pos,
                                    const int32_t *sel, int n_q, int B, int H, int max_blocks, int num_pages,
-                                   float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err) {
+                                   float scale, void *out, float *mass, bool implicit_local, int32_t *dev_err,
+                                   int fixed_seq, unsigned long long *mass_fx) {
     const long long grid = (long long)n_q * H;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[2];
@@ -400,7 +409,7 @@ cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8C
                                                    : sparse_attn_kv8_kernel<1>, (const uint2 *)q,
                               (const uint4 *)kv.k, (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, q_seq,
                               q_pos, sel, B, H, max_blocks, num_pages, scale * kLog2e, implicit_local ? 1 : 0,
-                              (__nv_bfloat16 *)out, mass, dev_err);
+                              fixed_seq, (__nv_bfloat16 *)out, mass, mass_fx, dev_err);
 }
 
 namespace {

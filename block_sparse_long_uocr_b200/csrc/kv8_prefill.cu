@@ -17,6 +17,7 @@
 //                each slot is added to its block's as a multiple of 2^-40 (integers: the sum does
 //                not depend on the order of the atomics);
 //   5. totals    the sums of step 4 added to the running totals.
+// A few queries are attended one by one instead (sparse_attn_kv8_kernel); their weights go the same way.
 // Roundings to fewer than 32 bits: the weights p in [0, 1] to fp16 for P V (2^-11 relative, their
 // sum l keeps 32 bits) and the partial outputs to fp16 (2^-11; |acc| <= 32 * 448, in units of the
 // block's value scale, so fp16 holds it): each an eighth of the output's own rounding to bf16.
@@ -41,7 +42,6 @@ namespace {
 constexpr int kRows = 16;        // entries of an item
 constexpr int kBlkWarps = 4, kBlkCtas = 4;
 constexpr int kMrgWarps = 8;
-constexpr float kMassUnit = 1.f / (1ll << 40);
 
 constexpr int kQStride = kD * 2 + 64;
 
@@ -510,8 +510,7 @@ kv8_merge_kernel(const int32_t *__restrict__ sel_ws, const uint4 *__restrict__ p
     to[0] = make_uint2(r[0], r[1]);
     to[4] = make_uint2(r[2], r[3]);
     if (mass_fx && some) {
-        const float share = finite_weight(w / L);   // in [0, 1]
-        atomicAdd(mass_fx + (size_t)h * max_blocks + j, (unsigned long long)__float2ull_rn(share / kMassUnit));
+        atomicAdd(mass_fx + (size_t)h * max_blocks + j, fixed_weight(w / L));
     }
 }
 
@@ -574,16 +573,32 @@ bool tile8_map(CUtensorMap *map, const void *cache, int num_pages, int H) {
 
 size_t prefill_kv8_workspace(int n_q, int H, int max_blocks) { return layout(n_q, H, max_blocks).total; }
 
-cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, int32_t **sched) {
+namespace {
+// Few rows: a query at a time (sparse_attn_kv8_kernel), as long as all its CTAs are resident at once.
+// The block by block form has five launches where that has one (three with totals), and reads a
+// block once where that reads it once per query.  Measured, blocks / queries (us, both with totals, 10
+// heads): over 4000 tokens 1 query 12.5 / 7.4, 16: 14.0 / 10.3, 50: 15.2 / 15.0, 74: 16.1 / 17.2, 100: 16.7 /
+// 25.6; over 60000 1: 13.6 / 7.6, 16: 17.8 / 10.8, 50: 25.1 / 16.5, 74: 27.1 / 19.1, 100: 29.4 / 30.1.
+bool per_query(const LaunchCtx &c, int n_q, int H) { return (long long)n_q * H <= 5ll * c.num_sms; }
+}  // namespace
+
+cudaError_t zero_prefill_kv8(const LaunchCtx &c, void *ws, int n_q, int H, int max_blocks, bool totals,
+                             int32_t **sched) {
     const Kv8PrefillWs w = layout(n_q, H, max_blocks);
-    if (sched) *sched = (int32_t *)((char *)ws + w.sched_off);
-    return cudaMemsetAsync(ws, 0, w.zero_bytes, c.stream);
+    char *base = (char *)ws;
+    if (sched) *sched = (int32_t *)(base + w.sched_off);
+    // what is needed: [counts, list counters], the scoring's counter, [sums]
+    const size_t from = !per_query(c, n_q, H) ? 0 : sched ? w.sched_off : w.mass_off;
+    const size_t to = totals ? w.zero_bytes : w.mass_off;
+    return from < to ? cudaMemsetAsync(base + from, 0, to - from, c.stream) : cudaSuccess;
 }
 
-cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt_row,
-                               const int32_t *seq_len_ptr, const int32_t *q_pos, const int32_t *sel, int n_q, int H,
-                               int max_blocks, int num_pages, float scale, void *out, float *mass_row, void *ws,
-                               int32_t *dev_err) {
+cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
+                               const int32_t *seq_lens, int seq, const int32_t *q_pos, const int32_t *sel, int n_q,
+                               int B, int H, int max_blocks, int num_pages, float scale, void *out, float *mass,
+                               void *ws, int32_t *dev_err) {
+    const int32_t *bt_row = bt + (size_t)seq * max_blocks, *seq_len_ptr = seq_lens + seq;
+    float *mass_row = mass ? mass + (size_t)seq * H * max_blocks : nullptr;
     const Kv8PrefillWs w = layout(n_q, H, max_blocks);
     char *base = (char *)ws;
     int32_t *counts = (int32_t *)(base + w.counts_off), *n_items = (int32_t *)(base + w.n_items_off);
@@ -601,6 +616,19 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     cudaLaunchConfig_t cfg = {};
     cfg.stream = c.stream;
     cfg.attrs = attr;
+    auto add_totals = [&]() {
+        const int n = H * max_blocks;
+        cfg.numAttrs = 1;
+        cfg.gridDim = dim3((unsigned)((n + 255) / 256));
+        cfg.blockDim = dim3(256);
+        return cudaLaunchKernelEx(&cfg, kv8_totals_kernel, (const unsigned long long *)mass_fx, n, mass_row);
+    };
+    if (per_query(c, n_q, H)) {
+        // (after the selection kernel of a whole step its slots have the layout that it gives them)
+        const cudaError_t e = launch_sparse_attn_kv8(c, q, kv, bt, seq_lens, nullptr, q_pos, sel, n_q, B, H, max_blocks,
+                                                     num_pages, scale, out, nullptr, c.pdl, dev_err, seq, mass_fx);
+        return e != cudaSuccess || !mass_row ? e : add_totals();
+    }
     cfg.numAttrs = c.pdl ? 1 : 0;
     const int n_rows = n_q * H, row_ctas = (n_rows + 15) / 16;   // below 2^30 rows
     cfg.gridDim = dim3((unsigned)(row_ctas + (n_q + 15) / 16));
@@ -631,11 +659,7 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     cfg.blockDim = dim3(kMrgWarps * 32);
     e = cudaLaunchKernelEx(&cfg, kv8_merge_kernel, (const int32_t *)sel_ws, (const uint4 *)part_o, (const float4 *)ml,
                            n_rows, H, max_blocks, (uint4 *)out, mass_fx);
-    if (e != cudaSuccess || !mass_row) return e;
-    const int n = H * max_blocks;
-    cfg.gridDim = dim3((unsigned)((n + 255) / 256));
-    cfg.blockDim = dim3(256);
-    return cudaLaunchKernelEx(&cfg, kv8_totals_kernel, (const unsigned long long *)mass_fx, n, mass_row);
+    return e != cudaSuccess || !mass_row ? e : add_totals();
 }
 
 }  // namespace uocr

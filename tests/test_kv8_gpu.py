@@ -171,12 +171,13 @@ def test_sparse_device_errors(uocr, cuda_device):
     check_rows(c, out, mass, [(1, 1, 299, left), (2, 2, 99, sel[2].tolist())])
 
 
+@pytest.mark.parametrize("H", [3, 40])       # few rows: a query at a time; many: block by block
 @pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-3])
-def test_any_finite_scale(uocr, cuda_device, scale):
+def test_any_finite_scale(uocr, cuda_device, scale, H):
     """A negative scale turns the order of the scores round, 0 makes them all equal (also next to tokens that are
     behind the query)."""
     n, total = 20, 150
-    c = Case([total], 3, seed=17, n_q=n)
+    c = Case([total], H, seed=17, n_q=n)
     pos = list(range(total - n, total))
     sel = torch.full((n, 16), -1, dtype=torch.int32)
     sel[:, 3:8] = torch.arange(5)
@@ -227,7 +228,11 @@ def test_pools_past_32_bit_offsets(uocr, cuda_device):
     rows = [(0, 0, total - 1, list(range(10)))]
     check_rows(c, uocr.sparse_attn_kv8(q, k8, v8, *scales, bt, sl, sel.to(cuda_device)), None, rows)
     check_rows(c, uocr.dense_decode_kv8(q, k8, v8, *scales, bt, sl), None, rows)
-    check_rows(c, uocr.sparse_attn_seq_kv8(q, k8, v8, *scales, bt, sl, 0, pos, sel.to(cuda_device)), None, rows, many=True)
+    for n in (1, 80):    # a query at a time, and block by block
+        out = uocr.sparse_attn_seq_kv8(q.expand(n, -1, -1).contiguous(), k8, v8, *scales, bt, sl, 0, pos.expand(n).contiguous(),
+                                       sel.to(cuda_device).expand(n, -1).contiguous())
+        check_rows(c, out, None, rows, many=True)
+        assert torch.equal(out, out[:1].expand(n, -1, -1))
     g = torch.Generator().manual_seed(1)
     for n in (1, 40):    # both of the append's forms
         rnd = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16)  # noqa: E731
@@ -318,9 +323,10 @@ def test_many_queries_of_a_sequence(uocr, cuda_device, total, n, H, order):
     check_rows(c, one, None, [(i, 0, pos[i], sel[i].tolist()) for i in range(n)])
 
 
-def test_many_queries_later_nan_does_not_reach_earlier_ones(uocr, cuda_device):
+@pytest.mark.parametrize("H", [2, 30])
+def test_many_queries_later_nan_does_not_reach_earlier_ones(uocr, cuda_device, H):
     """A token whose value is NaN is behind some queries of its block: theirs stay finite."""
-    c = Case([160], 2, seed=14, n_q=32)
+    c = Case([160], H, seed=14, n_q=32)
     pos = list(range(128, 160))
     c.v.view(torch.uint8)[int(c.table[0, 4]), 1, 20, 3] = 0xFF
     sel = torch.full((32, 16), -1, dtype=torch.int32)
@@ -334,22 +340,24 @@ def test_many_queries_later_nan_does_not_reach_earlier_ones(uocr, cuda_device):
     assert torch.isfinite(o).all()
 
 
-def test_many_queries_bad_slots_positions_and_pages(uocr, cuda_device):
-    c = Case([640], 2, seed=15, n_q=6)
-    pos = [639, 700, -1, 100, 5, 300]
-    sel = c.select([639, 639, 639, 100, 5, 300], 0.5)
-    sel[3] = torch.tensor([19, 3, 1, 3, -7] + [-1] * 11)       # 19: not causal; 3 twice
+@pytest.mark.parametrize("times", [1, 80])
+def test_many_queries_bad_slots_positions_and_pages(uocr, cuda_device, times):
+    c = Case([640], 2, seed=15, n_q=6 * times)
+    pos = [639, 700, -1, 100, 5, 300] * times
+    sel = c.select([639, 639, 639, 100, 5, 300] * times, 0.5)
     c.table[0, 2] = -5
-    sel[5] = torch.tensor([2, 4] + [-1] * 14)
+    for x in range(times):
+        sel[6 * x + 3] = torch.tensor([19, 3, 1, 3, -7] + [-1] * 11)       # 19: not causal; 3 twice
+        sel[6 * x + 5] = torch.tensor([2, 4] + [-1] * 14)
     q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
     err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
     mass = c.mass.to(cuda_device)
     out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device),
                                    mass=mass, dev_err=err)
     assert int(err) == uocr.DEVERR_SEL | uocr.DEVERR_PAGE | uocr.DEVERR_POS
-    assert (out[1:3].float() == 0).all()
+    assert all((out[6 * x + 1:6 * x + 3].float() == 0).all() for x in range(times))
     fine = lambda i: [j for j in sel[i].tolist() if 0 <= j <= pos[i] // BLOCK and j != 2]  # noqa: E731
-    check_rows(c, out, mass, [(i, 0, pos[i], fine(i)) for i in (0, 3, 4, 5)], many=True)
+    check_rows(c, out, mass, [(6 * x + i, 0, pos[i], fine(6 * x + i)) for x in range(times) for i in (0, 3, 4, 5)], many=True)
 
 
 # ------------------------------------------------------------------------------------------ append
