@@ -140,8 +140,6 @@ __device__ __forceinline__ int checked_page(const int32_t *bt_row, int j, int nu
 
 constexpr int kSWarps = 4;       // sparse: warps of a CTA
 constexpr int kDWarps = 4;       // dense: warps of a CTA, each every fourth block of its chunk
-constexpr int kMaxChunk = 16;    // dense: most blocks of a chunk
-constexpr size_t kFewChunks = 1480;   // dense: shorter chunks where there would be fewer CTAs than this
 constexpr int kMergeThreads = 512;
 
 }  // namespace
@@ -151,7 +149,8 @@ constexpr int kMergeThreads = 512;
 // through its shared memory: an SM takes in 64 bytes a clock, so the 128 KiB of a (query, head)
 // alone keep one for 1 us (one CTA of 16 warps took 7.0 us for 10 pairs, four CTAs 5.0).  With
 // enough pairs to fill the SMs one CTA does all 16.
-template <int kCluster>
+// kSeq: the queries are a chunk of one sequence.
+template <int kCluster, bool kSeq>
 __global__ void __launch_bounds__(kSWarps * 32, 5)
 sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
                        const float *__restrict__ k_scale, const float *__restrict__ v_scale,
@@ -177,8 +176,8 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
     const bool report = threadIdx.x == 0 && h == 0 && rank == 0;
-    bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err, report, r, fixed_seq);
-    if (fixed_seq >= 0 && ok && r.p < 0) {   // a chunk's positions are the caller's
+    bool ok = resolve_query(i, seq_lens, q_seq, q_pos, B, max_blocks, dev_err, report, r, kSeq ? fixed_seq : -1);
+    if (kSeq && ok && r.p < 0) {   // a chunk's positions are the caller's
         if (report) flag_error(dev_err, UOCR_DEVERR_POS);
         ok = false;
     }
@@ -203,7 +202,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     const Query8 query = split_query8(s_q[warp], raw, lane);   // while the page is on its way
     bl.j = bl.page >= 0 ? j : -1;
     load_scales8(bl, k_scale, v_scale, H, h);
-    float *const totals = mass ? mass + ((size_t)(ok ? r.b : 0) * H + h) * max_blocks : nullptr;
+    float *const totals = !kSeq && mass ? mass + ((size_t)(ok ? r.b : 0) * H + h) * max_blocks : nullptr;
     const float before = totals && bl.j >= 0 ? __ldcg(totals + bl.j) : 0.f;   // in flight beside the attention
 
     State8 st;
@@ -238,7 +237,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     if (rank == 0) {
         // L is 0 for a query without a visible token, NaN where a score is
         out[(size_t)ih * kD + d] = __float2bfloat16_rn(L != 0.f ? A / L : 0.f);
-        if ((totals || mass_fx) && warp == 0) {
+        if ((kSeq ? mass_fx != nullptr : totals != nullptr) && warp == 0) {
             // one writer per block: the first slot that names it adds the weights of all that do
             const int x = lane & 15;
             const int block = __float_as_int(s_slot[2][x]);
@@ -253,7 +252,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
                 w = all;
             }
             if (lane < kSel && block >= 0 && lane == __ffs(same) - 1 && L > 0.f) {
-                if (totals)
+                if (!kSeq)
                     totals[block] = s_slot[3][x] + finite_weight(w / L);
                 else   // many queries of one sequence: a sum of integers, in any order
                     atomicAdd(mass_fx + (size_t)h * max_blocks + block, fixed_weight(w / L));
@@ -265,7 +264,17 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     if (blockIdx.x == 0 && threadIdx.x == 0) pdl_wait();
 }
 
-// Split over chunks of blocks: CTA (query, head, chunk) leaves {m, l}, acc[128] and, for the
+// The blocks that a dense query attends, as one list: [0, pre) and [win, nb).
+struct Attended {
+    int nb, pre, win;
+    __device__ __forceinline__ Attended(int causal, int ref_blocks)
+        : nb(causal), pre(min(ref_blocks, causal)), win(max(causal - kLocal, min(ref_blocks, causal))) {}
+    __device__ __forceinline__ int count() const { return pre + nb - win; }
+    __device__ __forceinline__ int block(int t) const { return t < pre ? t : win + t - pre; }
+    __device__ __forceinline__ bool has(int j) const { return j < pre || (j >= win && j < nb); }
+};
+
+// Split over chunks of the list: CTA (query, head, chunk) leaves {m, l}, acc[128] and, for the
 // totals, each block's weight sum with the maximum it refers to.
 __global__ void __launch_bounds__(kDWarps * 32, 5)
 dense_kv8_chunk_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc, const uint4 *__restrict__ vc,
@@ -284,23 +293,21 @@ dense_kv8_chunk_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
     QueryRef r;
     const bool ok = resolve_query(i, seq_lens, nullptr, nullptr, B, max_blocks, dev_err,
                                   threadIdx.x == 0 && chunk == 0 && h == 0, r);
-    const int nb = ok ? r.nb : 0;
-    if (chunk * chunk_blocks >= nb) return;   // the merge reads only the chunks below nb
+    const Attended att(ok ? r.nb : 0, ref_blocks);
+    if (chunk * chunk_blocks >= att.count()) return;   // the merge reads only the chunks below that
 
-    const int j = chunk * chunk_blocks + warp + kDWarps * lane;   // of the lanes below chunk_blocks / 4
-    const bool mine = lane < chunk_blocks / kDWarps && j < nb;
+    const int t = chunk * chunk_blocks + warp + kDWarps * lane;   // of the lanes below chunk_blocks / 4
+    const bool mine = lane < chunk_blocks / kDWarps && t < att.count();
     Blocks8 bl;
-    bl.j = j;
-    bl.page = mine && (j < ref_blocks || j >= nb - kLocal)
-                  ? checked_page(bt + (size_t)r.b * max_blocks, j, num_pages, dev_err)
-                  : -1;
+    bl.j = mine ? att.block(t) : 0;
+    bl.page = mine ? checked_page(bt + (size_t)i * max_blocks, bl.j, num_pages, dev_err) : -1;
     const Query8 query = split_query8(s_q[warp], raw, lane);   // while the pages are on their way
     load_scales8(bl, k_scale, v_scale, H, h);
-    if (blk_ml && mine && bl.page < 0) blk_ml[(size_t)ih * max_blocks + j] = make_float2(-INFINITY, 0.f);
+    if (blk_ml && mine && bl.page < 0) blk_ml[(size_t)ih * max_blocks + bl.j] = make_float2(-INFINITY, 0.f);
     State8 st;
-    attend8(st, bl, kc, vc, H, h, ok ? r.p : -1, scale_log2, query, lane,
+    attend8(st, bl, kc, vc, H, h, __ldg(seq_lens + i) - 1, scale_log2, query, lane,
             [&](int t, float m, float l) {
-                if (blk_ml && lane == t) blk_ml[(size_t)ih * max_blocks + j] = make_float2(m, l);
+                if (blk_ml && lane == t) blk_ml[(size_t)ih * max_blocks + bl.j] = make_float2(m, l);
             });
     put_state8(s, st, warp, lane);
     __syncthreads();
@@ -316,8 +323,8 @@ dense_kv8_chunk_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
 // and four dims per lane; CTA (query, head, 1 + x) adds the weights of the blocks [512 x, 512 x + 512)
 // to their totals.
 __global__ void __launch_bounds__(kMergeThreads)
-dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int max_blocks, int chunk_blocks, int n_chunks,
-                       int parts, const float4 *__restrict__ part_acc, const float2 *__restrict__ part_ml,
+dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int max_blocks, int ref_blocks,
+                       int chunk_blocks, int n_chunks, int parts, const float4 *__restrict__ part_acc, const float2 *__restrict__ part_ml,
                        const float2 *__restrict__ blk_ml, __nv_bfloat16 *__restrict__ out, float *__restrict__ mass) {
     constexpr int kWarps = kMergeThreads / 32;
     __shared__ float s_red[kWarps];
@@ -326,11 +333,11 @@ dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int m
     const int i = ih / H, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     QueryRef r;
     const bool ok = resolve_query(i, seq_lens, nullptr, nullptr, B, max_blocks, nullptr, false, r);
-    const int nb = ok ? r.nb : 0;
-    const int used = (nb + chunk_blocks - 1) / chunk_blocks;
-    if (part > 0 && (part - 1) * kMergeThreads >= nb) return;
+    const Attended att(ok ? r.nb : 0, ref_blocks);
+    const int used = (att.count() + chunk_blocks - 1) / chunk_blocks;
+    if (part > 0 && (part - 1) * kMergeThreads >= att.nb) return;
     const int j = (part - 1) * kMergeThreads + tid;
-    const bool add = part > 0 && j < nb;
+    const bool add = part > 0 && att.has(j);
     const size_t at = (size_t)ih * max_blocks + j;
     const float before = add ? mass[at] : 0.f;   // not written by the kernel before this one
     pdl_wait();
@@ -404,9 +411,11 @@ cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8C
     cfg.stream = c.stream;
     cfg.attrs = cluster > 1 ? attr : attr + 1;
     cfg.numAttrs = (cluster > 1 ? 1 : 0) + (c.pdl ? 1 : 0);
-    return cudaLaunchKernelEx(&cfg, cluster == 4   ? sparse_attn_kv8_kernel<4>
-                                    : cluster == 2 ? sparse_attn_kv8_kernel<2>
-                                                   : sparse_attn_kv8_kernel<1>, (const uint2 *)q,
+    auto pick = [cluster](auto four, auto two, auto one) { return cluster == 4 ? four : cluster == 2 ? two : one; };
+    return cudaLaunchKernelEx(&cfg, fixed_seq >= 0 ? pick(sparse_attn_kv8_kernel<4, true>, sparse_attn_kv8_kernel<2, true>,
+                                                          sparse_attn_kv8_kernel<1, true>)
+                                                   : pick(sparse_attn_kv8_kernel<4, false>, sparse_attn_kv8_kernel<2, false>,
+                                                          sparse_attn_kv8_kernel<1, false>), (const uint2 *)q,
                               (const uint4 *)kv.k, (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, q_seq,
                               q_pos, sel, B, H, max_blocks, num_pages, scale * kLog2e, implicit_local ? 1 : 0,
                               fixed_seq, (__nv_bfloat16 *)out, mass, mass_fx, dev_err);
@@ -417,15 +426,28 @@ struct Dense8Ws {
     int chunk_blocks, n_chunks;
     size_t acc_off, ml_off, blk_off, total;
 };
-Dense8Ws dense8_layout(int n_q, int H, int max_blocks) {
+// Blocks of a chunk, by the CTAs that would come of it where every row attends all that it may.  Fewer
+// CTAs than are resident at once (740 on 148 SMs) leave SMs idle, so chunks get shorter; long ones
+// save prologues and partial states.  32 blocks only for one sequence: where several differ in
+// length, the longest one's last CTAs then run alone.  Measured (us, 10 heads) with 8 / 16 / 32 blocks: 1 x
+// 131072 tokens 64.9 / 61.9 / 59.9; 16 x 32768 - / 209 / 207; 40 x 500 .. 12000 - / 107 / 111; 3 x 100 .. 60000
+// 48.1 / 46.5 / 50.9; 16 x 4096 35.7 / 34.1 / -; 1 x 60000 with a prefix of 20 blocks, 4 / 16: 6.2 / 12.4.
+constexpr size_t kResident = 740;
+int dense8_chunk(int n_q, int H, int blocks) {
+    auto ctas = [&](int chunk) { return (size_t)n_q * H * ((blocks + chunk - 1) / chunk); };
+    if (n_q == 1 && ctas(32) >= kResident) return 32;
+    return ctas(16) >= kResident ? 16 : ctas(8) >= kResident ? 8 : 4;
+}
+Dense8Ws dense8_layout(int n_q, int H, int max_blocks, int ref_blocks) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     Dense8Ws w{};
     const size_t rows = (size_t)n_q * H;
-    w.chunk_blocks = kMaxChunk;
-    while (w.chunk_blocks > kDWarps && rows * ((max_blocks + w.chunk_blocks - 1) / w.chunk_blocks) < kFewChunks)
-        w.chunk_blocks /= 2;
-    w.n_chunks = (max_blocks + w.chunk_blocks - 1) / w.chunk_blocks;
-    const size_t slots = rows * w.n_chunks;
+    const int blocks = (int)min((long long)max_blocks, (long long)ref_blocks + kLocal);
+    w.chunk_blocks = dense8_chunk(n_q, H, blocks);
+    w.n_chunks = (blocks + w.chunk_blocks - 1) / w.chunk_blocks;
+    // chunks below 16 blocks are taken only where twice as long ones would be fewer than kResident: the
+    // workspace holds any ref_blocks
+    const size_t slots = max(rows * ((max_blocks + 15) / 16), rows + 2 * kResident);
     w.ml_off = up(slots * kD * 4);
     w.blk_off = w.ml_off + up(slots * sizeof(float2));
     w.total = w.blk_off + up(rows * max_blocks * sizeof(float2));
@@ -433,12 +455,12 @@ Dense8Ws dense8_layout(int n_q, int H, int max_blocks) {
 }
 }  // namespace
 
-size_t dense_kv8_workspace(int n_q, int H, int max_blocks) { return dense8_layout(n_q, H, max_blocks).total; }
+size_t dense_kv8_workspace(int n_q, int H, int max_blocks) { return dense8_layout(n_q, H, max_blocks, 0).total; }
 
 cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &kv, const int32_t *bt,
                              const int32_t *seq_lens, int B, int H, int max_blocks, int num_pages, int ref_blocks,
                              float scale, void *out, float *mass, void *ws, int32_t *dev_err) {
-    const Dense8Ws w = dense8_layout(B, H, max_blocks);
+    const Dense8Ws w = dense8_layout(B, H, max_blocks, ref_blocks);
     float *acc = (float *)((char *)ws + w.acc_off);
     float2 *ml = (float2 *)((char *)ws + w.ml_off);
     float2 *blk = mass ? (float2 *)((char *)ws + w.blk_off) : nullptr;
@@ -460,8 +482,8 @@ cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &
     cfg.blockDim = dim3(kMergeThreads);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, dense_kv8_merge_kernel, seq_lens, B, H, max_blocks, w.chunk_blocks,
-                              w.n_chunks, parts, (const float4 *)acc, (const float2 *)ml, (const float2 *)blk, (__nv_bfloat16 *)out, mass);
+    return cudaLaunchKernelEx(&cfg, dense_kv8_merge_kernel, seq_lens, B, H, max_blocks, ref_blocks,
+                              w.chunk_blocks, w.n_chunks, parts, (const float4 *)acc, (const float2 *)ml, (const float2 *)blk, (__nv_bfloat16 *)out, mass);
 }
 
 }  // namespace uocr
