@@ -244,8 +244,5 @@ __device__ __forceinline__ void st_cluster(uint32_t at, float v) {
 __device__ __forceinline__ void st_cluster(uint32_t at, uint64_t v) {
     asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
-__device__ __forceinline__ void red_cluster(uint32_t at, int v) {
-    asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
-}
 
 }  // namespace uocr

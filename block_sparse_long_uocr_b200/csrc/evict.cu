@@ -312,8 +312,8 @@ inline size_t one_smem(int H, int max_blocks, int ctas) {
 
 __global__ void __launch_bounds__(kOneThreads)
 evict_one_kernel(const float *mass, const int32_t *table, const int32_t *seq_lens, int H, int max_blocks,
-                 int keep_blocks, int n_sink, int ctas, int wide, int wide_out, float *new_mass, int32_t *new_table, int32_t *new_lens,
-                 int32_t *__restrict__ freed, int32_t *__restrict__ n_freed, int32_t *dev_err) {
+                 int keep_blocks, int n_sink, int ctas, int wide, int wide_out, float *new_mass, int32_t *new_table,
+                 int32_t *new_lens, int32_t *__restrict__ freed, int32_t *__restrict__ n_freed, int32_t *dev_err) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ OneSmem s;
     const int rank = cluster_rank(), b = blockIdx.x / ctas, tid = threadIdx.x;

@@ -9,7 +9,7 @@
 // free, so 22 bits of it are kept.
 //
 // The codes cannot go to the tensor cores as they are: mma.sync m16n8k32 on e4m3 operands runs on a
-// B200 as two fp16 MMAs and some 17 further instructions (counted: 19.9 issued per MMA with its
+// B200 as two fp16 MMAs and some 17 further instructions (counted: 23.6 issued per MMA with its
 // operand loads against 6.6 for the fp16 one), which converts every operand at every use.  Converted
 // once, a tile costs a lane 128 conversions (two codes each, 1.9 warp instructions a clock and SM)
 // and 32 MMAs (0.5 a clock).

@@ -324,8 +324,8 @@ dense_kv8_chunk_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
 // to their totals.
 __global__ void __launch_bounds__(kMergeThreads)
 dense_kv8_merge_kernel(const int32_t *__restrict__ seq_lens, int B, int H, int max_blocks, int ref_blocks,
-                       int chunk_blocks, int n_chunks, int parts, const float4 *__restrict__ part_acc, const float2 *__restrict__ part_ml,
-                       const float2 *__restrict__ blk_ml, __nv_bfloat16 *__restrict__ out, float *__restrict__ mass) {
+                       int chunk_blocks, int n_chunks, int parts, const float4 *__restrict__ part_acc,
+                       const float2 *__restrict__ part_ml, const float2 *__restrict__ blk_ml, __nv_bfloat16 *__restrict__ out, float *__restrict__ mass) {
     constexpr int kWarps = kMergeThreads / 32;
     __shared__ float s_red[kWarps];
     __shared__ float4 s_acc[kWarps][kD / 4];
@@ -412,13 +412,14 @@ cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8C
     cfg.attrs = cluster > 1 ? attr : attr + 1;
     cfg.numAttrs = (cluster > 1 ? 1 : 0) + (c.pdl ? 1 : 0);
     auto pick = [cluster](auto four, auto two, auto one) { return cluster == 4 ? four : cluster == 2 ? two : one; };
-    return cudaLaunchKernelEx(&cfg, fixed_seq >= 0 ? pick(sparse_attn_kv8_kernel<4, true>, sparse_attn_kv8_kernel<2, true>,
-                                                          sparse_attn_kv8_kernel<1, true>)
-                                                   : pick(sparse_attn_kv8_kernel<4, false>, sparse_attn_kv8_kernel<2, false>,
-                                                          sparse_attn_kv8_kernel<1, false>), (const uint2 *)q,
-                              (const uint4 *)kv.k, (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, q_seq,
-                              q_pos, sel, B, H, max_blocks, num_pages, scale * kLog2e, implicit_local ? 1 : 0,
-                              fixed_seq, (__nv_bfloat16 *)out, mass, mass_fx, dev_err);
+    auto kernel = fixed_seq >= 0 ? pick(sparse_attn_kv8_kernel<4, true>, sparse_attn_kv8_kernel<2, true>,
+                                        sparse_attn_kv8_kernel<1, true>)
+                                 : pick(sparse_attn_kv8_kernel<4, false>, sparse_attn_kv8_kernel<2, false>,
+                                        sparse_attn_kv8_kernel<1, false>);
+    return cudaLaunchKernelEx(&cfg, kernel, (const uint2 *)q, (const uint4 *)kv.k, (const uint4 *)kv.v, kv.k_scale,
+                              kv.v_scale, bt, seq_lens, q_seq, q_pos, sel, B, H, max_blocks, num_pages,
+                              scale * kLog2e, implicit_local ? 1 : 0, fixed_seq, (__nv_bfloat16 *)out, mass, mass_fx,
+                              dev_err);
 }
 
 namespace {
@@ -429,9 +430,10 @@ struct Dense8Ws {
 // Blocks of a chunk, by the CTAs that would come of it where every row attends all that it may.  Fewer
 // CTAs than are resident at once (740 on 148 SMs) leave SMs idle, so chunks get shorter; long ones
 // save prologues and partial states.  32 blocks only for one sequence: where several differ in
-// length, the longest one's last CTAs then run alone.  Measured (us, 10 heads) with 8 / 16 / 32 blocks: 1 x
-// 131072 tokens 64.9 / 61.9 / 59.9; 16 x 32768 - / 209 / 207; 40 x 500 .. 12000 - / 107 / 111; 3 x 100 .. 60000
-// 48.1 / 46.5 / 50.9; 16 x 4096 35.7 / 34.1 / -; 1 x 60000 with a prefix of 20 blocks, 4 / 16: 6.2 / 12.4.
+// length, the longest one's last CTAs then run alone.  Measured (us, 10 heads) with 8 / 16 / 32 blocks:
+// 1 x 131072 tokens 64.9 / 61.9 / 59.9; 16 x 32768 - / 209 / 207; 40 x 500 .. 12000 - / 107 / 111;
+// 3 x 100 .. 60000 48.1 / 46.5 / 50.9; 16 x 4096 35.7 / 34.1 / -; 1 x 60000 with a prefix of 20
+// blocks, 4 / 16: 6.2 / 12.4.
 constexpr size_t kResident = 740;
 int dense8_chunk(int n_q, int H, int blocks) {
     auto ctas = [&](int chunk) { return (size_t)n_q * H * ((blocks + chunk - 1) / chunk); };
@@ -476,14 +478,16 @@ cudaError_t launch_dense_kv8(const LaunchCtx &c, const void *q, const Kv8Cache &
     cfg.stream = c.stream;
     cudaError_t e = cudaLaunchKernelEx(&cfg, dense_kv8_chunk_kernel, (const uint2 *)q, (const uint4 *)kv.k,
                                        (const uint4 *)kv.v, kv.k_scale, kv.v_scale, bt, seq_lens, B, H, max_blocks,
-                                       num_pages, ref_blocks, w.chunk_blocks, w.n_chunks, scale * kLog2e, acc, ml, blk, dev_err);
+                                       num_pages, ref_blocks, w.chunk_blocks, w.n_chunks, scale * kLog2e, acc, ml, blk,
+                                       dev_err);
     if (e != cudaSuccess) return e;
     cfg.gridDim = dim3((unsigned)(B * H * parts));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, dense_kv8_merge_kernel, seq_lens, B, H, max_blocks, ref_blocks,
-                              w.chunk_blocks, w.n_chunks, parts, (const float4 *)acc, (const float2 *)ml, (const float2 *)blk, (__nv_bfloat16 *)out, mass);
+                              w.chunk_blocks, w.n_chunks, parts, (const float4 *)acc, (const float2 *)ml,
+                              (const float2 *)blk, (__nv_bfloat16 *)out, mass);
 }
 
 }  // namespace uocr

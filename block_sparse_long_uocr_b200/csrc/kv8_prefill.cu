@@ -143,9 +143,9 @@ kv8_prepare_kernel(const uint4 *__restrict__ q, const int32_t *__restrict__ sel,
 __global__ void __launch_bounds__(kBlkWarps * 32, kBlkCtas)
 kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                  const uint4 *__restrict__ q16, const float *__restrict__ unit, const float *__restrict__ k_scale,
-                 const float *__restrict__ v_scale, const int2 *__restrict__ list, const int4 *__restrict__ items, const int32_t *__restrict__ n_items,
-                 int H, int num_pages, float scale_log2, uint4 *__restrict__ part_o, float4 *__restrict__ part_ml,
-                 int32_t *dev_err) {
+                 const float *__restrict__ v_scale, const int2 *__restrict__ list, const int4 *__restrict__ items,
+                 const int32_t *__restrict__ n_items, int H, int num_pages, float scale_log2,
+                 uint4 *__restrict__ part_o, float4 *__restrict__ part_ml, int32_t *dev_err) {
     extern __shared__ uint8_t raw_smem[];
     __shared__ uint64_t s_bar[kBlkWarps][2];   // K and Q, V of the warp's unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -214,7 +214,9 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
     };
     uint32_t parity = 0;
-    bool dead = false;   // a wait ran out: what follows is left empty
+    // a wait ran out and what follows is left empty; K's copy still on its way: 1 none, 2 the unit's
+    // that follows (parity), 3 the unit's own (parity ^ 1)
+    int dead = 0;
 
     const int first = blockIdx.x * kBlkWarps + warp;
     Place at{first / H, first % H};
@@ -244,8 +246,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
 
         // ---- S: rows g, g + 8; tokens 8 nt + c, 8 nt + 4 + c
-        bool ok = !good || mbar_wait_timed(bar_k, parity, kWaitLimitNs, nullptr);
-        __syncwarp();
+        const bool ok_k = __all_sync(0xffffffffu, !good || mbar_wait_timed(bar_k, parity, kWaitLimitNs, nullptr));
         float s[4][4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -269,7 +270,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             }
         }
         __syncwarp();   // K and Q are read: the next unit's may land
-        if (!dead) issue_qk(rec1, at1.h, ea1, eb1);
+        if (!dead && ok_k) issue_qk(rec1, at1.h, ea1, eb1);
 
         // ---- causal mask, maxima, weights
         const int t0 = rec.x * kBlock;
@@ -343,8 +344,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
 
         // ---- O = P V8: rows g, g + 8; column n of MMA e is dim 16 n + e
-        ok = (!good || mbar_wait_timed(bar_v, parity, kWaitLimitNs, nullptr)) && ok;
-        ok = __all_sync(0xffffffffu, ok);
+        const bool ok = __all_sync(0xffffffffu, (!good || mbar_wait_timed(bar_v, parity, kWaitLimitNs, nullptr)) && ok_k);
         if (good) parity ^= 1;
         auto v_token = [&](int x) { return 8 * (x >> 1) + (x & 1 ? r0 ^ 4 : r0); };
         auto v_piece = [&](int x) { return ld_smem((x & 1 ? my_v ^ (4u * kD + 64u) : my_v) + 1024u * (x >> 1)); };
@@ -416,7 +416,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         __syncwarp();   // V is read: the next unit's may land
         if (!ok) {      // a copy did not arrive in time: nothing of this unit and of those after it is kept
             if (lane == 0 && !dead) flag_error(dev_err, UOCR_DEVERR_TIMEOUT);
-            dead = true;
+            if (!dead) dead = !ok_k ? 3 : page_ok(rec1) ? 2 : 1;
         }
         if (!dead) issue_v(rec1, at1.h);
 
@@ -439,7 +439,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         rec2 = load_rec(at2);
     }
     if (dead) {   // copies still on their way end before the shared memory goes
-        mbar_drain(bar_k, parity, dev_err);
+        if (dead > 1) mbar_drain(bar_k, dead == 2 ? parity : parity ^ 1, dev_err);
         mbar_drain(bar_v, parity ^ 1, dev_err);
     }
 }
