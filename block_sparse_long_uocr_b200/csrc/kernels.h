@@ -15,8 +15,8 @@ struct LaunchCtx {
     int num_sms;
     bool pdl;   // launch with programmatic stream serialization
     // Limit of the first bounded wait of the decode attention (its V copy) and of the scoring
-    // GEMM's epilogue (its first accumulator); kWaitLimitNs except when a test shortens it to
-    // exercise the timeout path.  Every other wait keeps kWaitLimitNs.
+    // GEMM's epilogue (its first accumulator), and of the waits for K in the prefill attention over
+    // the 8-bit cache; kWaitLimitNs except when a test shortens it to exercise the timeout path.  Every other wait keeps kWaitLimitNs.
     uint64_t first_wait_ns;
 };
 

@@ -145,7 +145,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
                  const uint4 *__restrict__ q16, const float *__restrict__ unit, const float *__restrict__ k_scale,
                  const float *__restrict__ v_scale, const int2 *__restrict__ list, const int4 *__restrict__ items,
                  const int32_t *__restrict__ n_items, int H, int num_pages, float scale_log2,
-                 uint4 *__restrict__ part_o, float4 *__restrict__ part_ml, int32_t *dev_err) {
+                 uint4 *__restrict__ part_o, float4 *__restrict__ part_ml, int32_t *dev_err, uint64_t first_wait_ns) {
     extern __shared__ uint8_t raw_smem[];
     __shared__ uint64_t s_bar[kBlkWarps][2];   // K and Q, V of the warp's unit
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
@@ -246,7 +246,7 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         }
 
         // ---- S: rows g, g + 8; tokens 8 nt + c, 8 nt + 4 + c
-        const bool ok_k = __all_sync(0xffffffffu, !good || mbar_wait_timed(bar_k, parity, kWaitLimitNs, nullptr));
+        const bool ok_k = __all_sync(0xffffffffu, !good || mbar_wait_timed(bar_k, parity, first_wait_ns, nullptr));
         float s[4][4];
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
@@ -651,7 +651,7 @@ cudaError_t launch_prefill_kv8(const LaunchCtx &c, const void *q, const Kv8Cache
     cfg.dynamicSmemBytes = kSmem;
     e = cudaLaunchKernelEx(&cfg, kv8_block_kernel, map_k, map_v, (const uint4 *)q16, (const float *)unit, kv.k_scale,
                            kv.v_scale, (const int2 *)list, (const int4 *)items, (const int32_t *)n_items, H, num_pages,
-                           scale * kLog2e, part_o, ml, dev_err);
+                           scale * kLog2e, part_o, ml, dev_err, c.first_wait_ns);
     if (e != cudaSuccess) return e;
     cfg.dynamicSmemBytes = 0;
 

@@ -1,5 +1,6 @@
 """The operators over the 8-bit key / value cache against plain 64-bit forms (tests/kv8_util.py, which
 also derives the bounds), through the binding."""
+import ctypes
 import math
 
 import numpy as np
@@ -358,6 +359,38 @@ def test_many_queries_bad_slots_positions_and_pages(uocr, cuda_device, times):
     assert all((out[6 * x + 1:6 * x + 3].float() == 0).all() for x in range(times))
     fine = lambda i: [j for j in sel[i].tolist() if 0 <= j <= pos[i] // BLOCK and j != 2]  # noqa: E731
     check_rows(c, out, mass, [(6 * x + i, 0, pos[i], fine(6 * x + i)) for x in range(times) for i in (0, 3, 4, 5)], many=True)
+
+
+def test_many_queries_wait_timeout_is_flagged_and_recovers(uocr, cuda_device):
+    """The waits for the keys give up at once: every block is dropped and flagged, the copies are waited
+    for before their shared memory goes, and the next call is whole."""
+    case = Case([32 * 200], 10, seed=71, n_q=100)
+    positions = torch.arange(6000, 6100, dtype=torch.int32)
+    sel = case.select(positions.tolist())
+    q, k, v, ks, vs, table, sl = case.gpu(cuda_device)
+    pos, s = to(cuda_device, positions, sel)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+
+    def run():
+        (mass,) = to(cuda_device, case.mass)
+        out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, table, sl, 0, pos, s, mass=mass, dev_err=err)
+        torch.cuda.synchronize()
+        return out, mass
+
+    limit = uocr.lib.uocr_test_first_wait_limit_ns
+    limit.argtypes, limit.restype = [ctypes.c_longlong], None
+    limit(0)
+    try:
+        out, mass = run()
+    finally:
+        limit(-1)
+    assert int(err.item()) & uocr.DEVERR_TIMEOUT
+    assert (out == 0).all() and torch.equal(mass.cpu(), case.mass)
+    err.zero_()
+    out, mass = run()
+    assert int(err.item()) == 0
+    rows = [(i, 0, int(positions[i]), sel[i].tolist()) for i in range(100)]
+    check_rows(case, out, mass, rows, many=True)
 
 
 # ------------------------------------------------------------------------------------------ append
