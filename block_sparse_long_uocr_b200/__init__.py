@@ -670,6 +670,14 @@ def _space(workspace, nbytes, dev: int):
     return workspace
 
 
+def _lend(stream, *tensors):
+    """For a call on a stream other than the current one, whose tensors were allocated here: their memory is not
+    given out again before that stream is done with it."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(stream)
+
+
 def _check_dev_err(dev_err, dev: int):
     _dev(dev_err, "dev_err", _I32)
     if dev_err.numel() < 1 or dev_err.get_device() != dev:
@@ -817,6 +825,7 @@ def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             _at(q_seq), _at(q_pos), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
             out.data_ptr(), _at(mass), _at(dev_err))
+    _lend(stream, out)
     return out
 
 
@@ -831,6 +840,7 @@ def sparse_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache,
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), B, H, mb, P, out.data_ptr(), sel.data_ptr(), _at(mass),
             workspace.data_ptr(), workspace.numel(), _at(dev_err))
+    _lend(stream, out, sel, workspace)
     return out, sel
 
 
@@ -846,6 +856,7 @@ def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             mb if ref_blocks is None else int(ref_blocks), B, H, mb, P, out.data_ptr(), _at(mass),
             workspace.data_ptr(), workspace.numel(), _at(dev_err))
+    _lend(stream, out, workspace)
     return out
 
 
@@ -862,6 +873,7 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             int(seq), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
             out.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
+    _lend(stream, out, workspace)
     return out
 
 
@@ -877,6 +889,7 @@ def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), int(seq), q_pos.data_ptr(), n_q, B, H, mb, P, out.data_ptr(),
             sel.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
+    _lend(stream, out, sel, workspace)
     return out, sel
 
 
@@ -925,4 +938,5 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
             seq_lens.data_ptr(), B, H, mb, int(keep_blocks), int(n_sink), new_mass.data_ptr(), new_table.data_ptr(),
             new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), workspace.data_ptr(), workspace.numel(),
             _at(dev_err))
+    _lend(stream, new_mass, new_table, new_lens, freed, n_freed, workspace)
     return new_mass, new_table, new_lens, freed, n_freed

@@ -709,6 +709,36 @@ def test_captured_replayed_and_on_another_stream(uocr, cuda_device):
             assert torch.equal(a, b)
 
 
+def test_memory_of_a_call_on_another_stream_is_not_given_out(uocr, cuda_device, monkeypatch):
+    """A call on a given stream that allocates for itself: the workspace that it drops and outputs that the caller
+    drops stay taken until that stream has run it."""
+    c = Case([2000], 10, seed=35)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    spaces = []
+    real = uocr._space
+
+    def spy(*args):
+        t = real(*args)
+        spaces.append((t.data_ptr(), t.numel()))
+        return t
+
+    monkeypatch.setattr(uocr, "_space", spy)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(50_000_000)
+    out = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, stream=side)
+    at, size = spaces[0]
+    dropped = out.data_ptr()
+    del out
+    again = torch.empty(size, dtype=torch.uint8, device=cuda_device)
+    other = torch.empty_like(q)
+    busy = not side.query()
+    side.synchronize()
+    assert busy, "the stream was done before the allocations"
+    assert again.data_ptr() != at and other.data_ptr() != dropped
+
+
 def test_prompt_decode_evict_decode(uocr, cuda_device):
     """The operators as a server uses them: a prompt appended and attended in two chunks, decode steps, an eviction in
     place, pages freed, more decode steps on the shorter table; every attention against the 64-bit form on the cache
