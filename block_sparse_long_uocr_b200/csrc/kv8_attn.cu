@@ -427,18 +427,19 @@ struct Dense8Ws {
     int chunk_blocks, n_chunks;
     size_t acc_off, ml_off, blk_off, total;
 };
-// Blocks of a chunk, by the CTAs that would come of it where every row attends all that it may.  Fewer
-// CTAs than are resident at once (740 on 148 SMs) leave SMs idle, so chunks get shorter; long ones
-// save prologues and partial states.  32 blocks only for one sequence: where several differ in
-// length, the longest one's last CTAs then run alone.  Measured (us, 10 heads) with 8 / 16 / 32 blocks:
-// 1 x 131072 tokens 64.9 / 61.9 / 59.9; 16 x 32768 - / 209 / 207; 40 x 500 .. 12000 - / 107 / 111;
-// 3 x 100 .. 60000 48.1 / 46.5 / 50.9; 16 x 4096 35.7 / 34.1 / -; 1 x 60000 with a prefix of 20
-// blocks, 4 / 16: 6.2 / 12.4.
+// Blocks of a chunk, by the CTAs that would come of it where every row attends all that it may: the
+// shortest whose CTAs are all resident at once (740 on 148 SMs), for more warps on the same bytes; past
+// that 16, for fewer prologues and partial states.  32 blocks only for one sequence: where several
+// differ in length, the longest one's last CTAs then run alone.  Measured (us, 10 heads) with 4 / 8 / 16 / 32
+// blocks: 1 x 16384 tokens 17.2 / 14.7 / 14.0 / -; 5 x <= 9001 with a prefix of 100 blocks 14.1 / 13.2 /
+// 14.7 / -; 1 x 60000 with one of 20 6.2 / - / 12.4 / -; 4 x 8192 - / 21.2 / 19.4 / -; 16 x 4096 - / 35.7 / 34.1 / -;
+// 1 x 131072 - / 64.9 / 61.9 / 59.9; 16 x 32768 - / - / 209 / 207; 40 x 500 .. 12000 - / - / 107 / 111;
+// 3 x 100 .. 60000 - / 48.1 / 46.5 / 50.9.
 constexpr size_t kResident = 740;
 int dense8_chunk(int n_q, int H, int blocks) {
     auto ctas = [&](int chunk) { return (size_t)n_q * H * ((blocks + chunk - 1) / chunk); };
     if (n_q == 1 && ctas(32) >= kResident) return 32;
-    return ctas(16) >= kResident ? 16 : ctas(8) >= kResident ? 8 : 4;
+    return ctas(4) <= kResident ? 4 : ctas(8) <= kResident ? 8 : 16;
 }
 Dense8Ws dense8_layout(int n_q, int H, int max_blocks, int ref_blocks) {
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -447,9 +448,8 @@ Dense8Ws dense8_layout(int n_q, int H, int max_blocks, int ref_blocks) {
     const int blocks = (int)min((long long)max_blocks, (long long)ref_blocks + kLocal);
     w.chunk_blocks = dense8_chunk(n_q, H, blocks);
     w.n_chunks = (blocks + w.chunk_blocks - 1) / w.chunk_blocks;
-    // chunks below 16 blocks are taken only where twice as long ones would be fewer than kResident: the
-    // workspace holds any ref_blocks
-    const size_t slots = max(rows * ((max_blocks + 15) / 16), rows + 2 * kResident);
+    // chunks below 16 blocks are taken for kResident CTAs at most: the workspace holds any ref_blocks
+    const size_t slots = max(rows * ((max_blocks + 15) / 16), kResident);
     w.ml_off = up(slots * kD * 4);
     w.blk_off = w.ml_off + up(slots * sizeof(float2));
     w.total = w.blk_off + up(rows * max_blocks * sizeof(float2));

@@ -404,6 +404,9 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  * additions is fixed (integers where many queries meet): the same call gives the
  * same bits.  Weights that are not finite (a query or key with infinities or
  * NaN) add nothing.  Two calls that overlap on the GPU must not share a mass.
+ *
+ * Workspaces: as elsewhere (no contents needed, reusable by the next call on the
+ * stream, undefined afterwards: parts of them may be dropped from L2 unwritten).
  */
 
 /*
@@ -423,8 +426,8 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  *   s = need, if the page holds no older row of the sequence, else
  *       max(s_old rounded up to a power of two, need);
  * a new value x is stored as e4m3(x / s), and where s != s_old the older rows'
- * codes c become e4m3(c * s_old / s).  Rounding is to nearest even, once, from
- * the value in 64 bits; infinities and NaN are stored as NaN.  Rows of the
+ * codes c become e4m3(c * s_old / s), s_old finite.  Rounding is to nearest even,
+ * once, from the value in 64 bits; infinities and NaN are stored as NaN.  Rows of the
  * page behind the sequence's end keep what they hold.
  * A page must not receive tokens from two sequences in one call.  A sequence
  * whose new_start is not as above, with more new tokens than seq_lens, or
@@ -480,9 +483,12 @@ uocr_status_t uocr_dense_decode_kv8(const void *q, const void *k_cache, const vo
  * uocr_sparse_attn_seq over the 8-bit cache: n_q queries of sequence `seq`,
  * each over its own selection, every selected (block, head) tile read once for
  * all of them.  The softmax weights go to the tensor cores in fp16 and each
- * slot's partial output is kept in fp16 (2^-12 relative each); weight sums stay
- * fp32.  With mass, row `seq` receives the sum over the n_q queries.  Errors as
- * uocr_sparse_attn_seq.  Workspace: uocr_sparse_attn_seq_kv8_workspace_bytes.
+ * slot's partial output is kept in fp16 (2^-11 relative each); weight sums stay
+ * fp32.  A few queries (n_q * H up to 5 per SM) are attended one by one, as in
+ * uocr_sparse_attn_kv8.  With mass, row `seq` receives the sum over the n_q
+ * queries, each weight as a multiple of 2^-40; n_q above 2^23 is then
+ * UOCR_ERR_UNSUPPORTED, and so is num_pages * H above 2^31 - 1 with or without.
+ * Errors as uocr_sparse_attn_seq.  Workspace: uocr_sparse_attn_seq_kv8_workspace_bytes.
  */
 size_t uocr_sparse_attn_seq_kv8_workspace_bytes(int n_q, int H, int max_blocks);
 uocr_status_t uocr_sparse_attn_seq_kv8(const void *q, const void *k_cache, const void *v_cache, const float *k_scale,
