@@ -389,7 +389,7 @@ evict_one_kernel(const float *mass, const int32_t *table, const int32_t *seq_len
     if (take > 0) t = octave_threshold(s, keys, c0, c1, take);
     const int edge = s.bin;
     // whether a column stays whatever the ties are, and whether it is one of them
-    auto judge = [&](int j, bool &keep, bool &tie) {
+    auto decide = [&](int j, bool &keep, bool &tie) {
         keep = j < max_blocks;
         tie = false;
         if (j < c0 || j >= c1) return;
@@ -402,7 +402,7 @@ evict_one_kernel(const float *mass, const int32_t *table, const int32_t *seq_len
     int kept = 0, ties = 0;
     for (int j = tid; j < min(j0, max_blocks); j += kOneThreads) {
         bool keep, tie;
-        judge(j, keep, tie);
+        decide(j, keep, tie);
         kept += keep;
         ties += tie;
     }
@@ -418,7 +418,7 @@ evict_one_kernel(const float *mass, const int32_t *table, const int32_t *seq_len
         bool keep[2] = {false, false}, tie[2] = {false, false};
 #pragma unroll
         for (int y = 0; y < 2; ++y)
-            if (x + y < n) judge(j0 + x + y, keep[y], tie[y]);
+            if (x + y < n) decide(j0 + x + y, keep[y], tie[y]);
         int tot;
         if (!t.all) {   // uniform over the cluster
             const int before = ties + block_scan(tie[0] + tie[1], s.w, tot);

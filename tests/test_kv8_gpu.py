@@ -585,6 +585,22 @@ def test_evict_tables_beyond_shared_memory(uocr, cuda_device, H, in_place):
             assert torch.equal(w, x), (name, keep, sink)
 
 
+@pytest.mark.parametrize("mb,H", [(12000, 10), (16003, 4), (700, 64)])
+def test_evict_on_the_largest_clusters(uocr, cuda_device, mb, H):
+    """Tables of which only an eighth (a half, for many heads) fits in a CTA's shared memory."""
+    g = torch.Generator().manual_seed(mb)
+    mass = torch.exp(2 * torch.randn((2, H, mb), generator=g))
+    mass[1] = torch.randint(0, 2, (H, mb), generator=g).float()
+    table = torch.randint(0, 1 << 20, (2, mb), generator=g, dtype=torch.int32)
+    lens = torch.tensor([mb * BLOCK - 40, mb * BLOCK], dtype=torch.int32)
+    for keep, sink in ((mb // 4, 4), (mb - 3, 0)):
+        want = ref.evict(mass, table, lens, keep, sink)
+        got, err = run_evict(uocr, cuda_device, mass, table, lens, keep, sink, True)
+        assert err == 0
+        for w, x, name in zip(want, got, ("mass", "table", "lens", "freed", "n_freed")):
+            assert torch.equal(w, x), (name, keep, sink)
+
+
 def test_evict_bad_lengths_copy_and_flag(uocr, cuda_device):
     mass, table = torch.rand((3, 2, 50)), torch.arange(150, dtype=torch.int32).reshape(3, 50)
     lens = torch.tensor([-1, 50 * BLOCK + 1, 1000], dtype=torch.int32)
