@@ -725,6 +725,55 @@ def test_captured_replayed_and_on_another_stream(uocr, cuda_device):
             assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("n", [20, 150])     # a query at a time; block by block
+def test_prefill_and_decode_captured_and_replayed_on_new_contents(uocr, cuda_device, n):
+    """Two graphs on one workspace, replayed in turn after the queries, caches and lengths have changed."""
+    H, total = 10, 3000
+    c, other = Case([total, 777], H, seed=61, n_q=n), Case([total - 200, 900], H, seed=62, n_q=n, max_blocks=94)
+    assert c.mb == other.mb and c.k.shape[0] >= other.k.shape[0]
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    g = torch.Generator().manual_seed(63)
+    iq, ik = (torch.randn(s, generator=g).to(torch.bfloat16).to(cuda_device) for s in ((n, 128), (k.shape[0], 32, 128)))
+    pos = torch.arange(total - n - 200, total - 200, dtype=torch.int32, device=cuda_device)
+    mass = torch.zeros((2, H, c.mb), device=cuda_device)
+    ws = torch.empty(uocr.prefill_kv8_workspace_bytes(n, H, c.mb), dtype=torch.uint8, device=cuda_device)
+    out, sel = torch.empty_like(q), torch.empty((n, 16), dtype=torch.int32, device=cuda_device)
+    dout, dsel = torch.empty_like(q[:2]), torch.empty_like(sel[:2])
+    dws = torch.empty(uocr.workspace_bytes(2, H, c.mb), dtype=torch.uint8, device=cuda_device)
+
+    def step():
+        uocr.sparse_prefill_kv8(q, k, v, ks, vs, iq, ik, bt, sl, 0, pos, out=out, sel=sel, mass=mass, workspace=ws)
+        uocr.sparse_decode_kv8(q[:2], k, v, ks, vs, iq[:2], ik, bt, sl, out=dout, sel=dsel, mass=mass, workspace=dws)
+
+    graphs = []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            step()
+    for case in (c, other, c):
+        pages = case.k.shape[0]
+        for have, want in ((q, case.q), (k[:pages], case.k), (v[:pages], case.v), (ks[:pages], case.ks), (vs[:pages], case.vs), (bt, case.table),
+                           (sl, case.sl)):
+            have.copy_(want)
+        mass.zero_()
+        step()
+        torch.cuda.synchronize()
+        want = [x.clone() for x in (out, sel, dout, dsel, mass)]
+        for graph in graphs:
+            mass.zero_()
+            for x in (out, sel, dout, dsel):
+                x.zero_()
+            graph.replay()
+            torch.cuda.synchronize()
+            for a, b in zip(want, (out, sel, dout, dsel, mass)):
+                assert torch.equal(a, b)
+    base = total - n - 200
+    rows = [(i, 0, base + i, want[1][i].tolist()) for i in range(n)]
+    case = Case([total, 777], H, seed=61, n_q=n)
+    check_rows(case, want[0], None, rows, many=True)
+    assert abs(float(mass[0].sum()) - H * (n + 1)) < 1e-3 * H * (n + 1)
+
+
 def test_memory_of_a_call_on_another_stream_is_not_given_out(uocr, cuda_device, monkeypatch):
     """A call on a given stream that allocates for itself: the workspace that it drops and outputs that the caller
     drops stay taken until that stream has run it."""
