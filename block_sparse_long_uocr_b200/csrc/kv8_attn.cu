@@ -147,7 +147,7 @@ constexpr int kMergeThreads = 512;
 // A cluster of kCluster CTAs of 4 warps per (query, head); warp w of CTA r attends the selection slots
 // 4 r + w, + 4 kCluster, ...  With four CTAs every warp has one block, and the four meet in CTA 0
 // through its shared memory: an SM takes in 64 bytes a clock, so the 128 KiB of a (query, head)
-// alone keep one for 1 us (one CTA of 16 warps took 7.0 us for 10 pairs, four CTAs 5.0).  With
+// alone keep one for 1 us (10 pairs take 6.9 us with one CTA each, 4.6 with four).  With
 // enough pairs to fill the SMs one CTA does all 16.
 // kSeq: the queries are a chunk of one sequence.
 template <int kCluster, bool kSeq>
@@ -400,10 +400,12 @@ cudaError_t launch_sparse_attn_kv8(const LaunchCtx &c, const void *q, const Kv8C
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    // As many CTAs per pair as can all be resident at once, 5 a SM.  Measured with 1 / 2 / 4 (us; 148
-    // SMs): 10 pairs 7.2 / 6.1 / 5.0, 140: 10.8 / 9.0 / 8.5, 200: 11.9 / 10.0 / 14.6, 300: 13.8 /
-    // 12.7 / 16.7, 450: 15.4 / 20.0 / 22.9.
-    const int cluster = 4 * grid <= 5 * c.num_sms ? 4 : 2 * grid <= 5 * c.num_sms ? 2 : 1;
+    // As many CTAs per pair as can all be resident at once, 5 a SM; clusters of 4 do not fill every GPC to
+    // its last slot (176 pairs no longer fit on 148 SMs, and how many do depends on the GPCs), so for them
+    // 4.5.  Measured with 1 / 2 / 4 (us; 148 SMs): 10 pairs 6.9 / 5.7 / 4.6, 140: 10.5 / 8.3 / 7.6, 160: 10.9 /
+    // 8.7 / 8.3, 175: 11.1 / 8.8 / 8.3, 176: 11.0 / 8.7 / 11.0, 300: 12.2 / 11.5 / 14.9, 370: 13.5 / 13.1 /
+    // 19.2, 450: 14.9 / 19.1 / 21.1.
+    const int cluster = 8 * grid <= 9 * c.num_sms ? 4 : 2 * grid <= 5 * c.num_sms ? 2 : 1;
     attr[0].val.clusterDim.x = cluster;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(cluster * grid));
