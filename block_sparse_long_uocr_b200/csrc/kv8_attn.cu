@@ -172,7 +172,8 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
 
     // the selection, the query and the lengths are on their way before any of them is used
     const int32_t *my_sel = sel + (size_t)i * kSel + slot;
-    int j = implicit_local ? -2 : ld_pinned(my_sel);
+    // -2: not known yet; a caller's slot below 0 is empty, whatever its value
+    int j = implicit_local ? -2 : max(ld_pinned(my_sel), -1);
     const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
     const bool report = threadIdx.x == 0 && h == 0 && rank == 0;

@@ -361,6 +361,42 @@ def test_many_queries_bad_slots_positions_and_pages(uocr, cuda_device, times):
     check_rows(c, out, mass, [(6 * x + i, 0, pos[i], fine(6 * x + i)) for x in range(times) for i in (0, 3, 4, 5)], many=True)
 
 
+@pytest.mark.parametrize("empty", [-2, -1, -3, -(1 << 31)])
+def test_any_negative_slot_is_empty(uocr, cuda_device, empty):
+    """Slots below 0 in every place of the selection, of queries with at most 16 causal blocks and with more: through
+    the decode form and through both forms of many queries."""
+    H, lens = 10, [200, 1000]
+    for b, total in enumerate(lens):
+        for n in (5, 100):      # n * H up to 5 a SM: a query at a time; more: block by block
+            c = Case(lens, H, seed=90 + b, n_q=n)
+            pos = [total - 1 - (7 * i) % 130 for i in range(n)]
+            sel = torch.full((n, 16), empty, dtype=torch.int32)
+            for i, p in enumerate(pos):
+                nb = p // BLOCK + 1
+                if i % 5 == 1:                                     # 12 .. 15 empty
+                    sel[i, :3] = torch.tensor([nb - 1, 0, nb // 2])
+                elif i % 5 == 2:                                   # below 12 empty
+                    sel[i, 12:14] = torch.tensor([nb - 1, 0])
+                elif i % 5 == 3:
+                    sel[i, ::3] = torch.tensor([nb - 1, 0, nb // 2, empty, 1, empty])
+                elif i % 5 == 4:
+                    sel[i, 5] = nb - 1                             # (i % 5 == 0: nothing is selected)
+            q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+            qp, se = torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device)
+            rows = [(i, b, pos[i], sel[i].tolist()) for i in range(n)]
+            mass = c.mass.to(cuda_device)
+            check_rows(c, uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, b, qp, se, mass=mass), mass, rows, many=True)
+            seq = torch.full((n,), b, dtype=torch.int32, device=cuda_device)
+            check_rows(c, uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, se, seq, qp), None, rows)
+    c = Case(lens, H, seed=92)  # a query per sequence, with totals
+    sel = torch.full((2, 16), empty, dtype=torch.int32)
+    sel[0, 2], sel[1, 13] = 1, 30
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel.to(cuda_device), mass=mass)
+    check_rows(c, out, mass, [(i, i, lens[i] - 1, sel[i].tolist()) for i in range(2)])
+
+
 def test_many_queries_wait_timeout_is_flagged_and_recovers(uocr, cuda_device):
     """The waits for the keys give up at once: every block is dropped and flagged, the copies are waited
     for before their shared memory goes, and the next call is whole."""
