@@ -277,7 +277,9 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         const int far = __reduce_max_sync(0xffffffffu, max(ea.y, eb.y)) - t0 + 1;
         const int near = __reduce_min_sync(0xffffffffu, min(ea.y, eb.y)) - t0 + 1;
         // z = s fa (rows g), s fb: the maximum is taken over s, whose sign the factors then do not change,
-        // and each weight is one product and one exponential, 2^(s fa - ma)
+        // and a weight is 2^((s - max) fa): 1 at the maximum and at most 1 elsewhere, however large the
+        // scores are.  (2^(s fa - ma) with the product kept exact is one instruction less, but its exponent
+        // at the maximum is the rounding of ma: from scores of 2^27 on that leaves fp16's range.)
         ks *= scale_log2;
         if (ks < 0.f) {   // a negative scale
 #pragma unroll
@@ -314,16 +316,17 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
             mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
         }
         // the states' units are 2^ma, 2^mb (every score NaN or -inf: 2^0, and the sums say which)
-        ma = ma == -INFINITY ? 0.f : ma * fa;
-        mb = mb == -INFINITY ? 0.f : mb * fb;
+        const float sa = ma == -INFINITY ? 0.f : ma, sb = mb == -INFINITY ? 0.f : mb;
+        ma = sa * fa;
+        mb = sb * fb;
         uint32_t pa[4], pb[4];
 #pragma unroll
         for (int nt = 0; nt < 4; ++nt) {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                p[e] = exp2_approx(fmaf(s[nt][e], fa, -ma));
-                p[2 + e] = exp2_approx(fmaf(s[nt][2 + e], fb, -mb));
+                p[e] = exp2_approx((s[nt][e] - sa) * fa);
+                p[2 + e] = exp2_approx((s[nt][2 + e] - sb) * fb);
             }
             if (partly) {   // (-inf times a scale of 0 is not -inf)
 #pragma unroll

@@ -397,6 +397,39 @@ def test_any_negative_slot_is_empty(uocr, cuda_device, empty):
     check_rows(c, out, mass, [(i, i, lens[i] - 1, sel[i].tolist()) for i in range(2)])
 
 
+@pytest.mark.parametrize("n", [5, 100])      # a query at a time; block by block
+@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-3, 30.0, 1e7, 1e8, 1e9, 1e20])
+def test_many_queries_of_any_magnitude(uocr, cuda_device, n, q_scale):
+    """From a flat softmax to scores far past 2^31: where the highest score leads by more than the products' error
+    (ref.weight_bound: 2^-18 of the sum of magnitudes each) and 2^10, the output is that token's value."""
+    H, total, scale = 10, 700, 128 ** -0.5
+    c = Case([total], H, seed=93, n_q=n, q_scale=q_scale)
+    pos = [total - 1 - 3 * (i % 70) for i in range(n)]
+    sel = c.select(pos)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, torch.tensor(pos, dtype=torch.int32, device=cuda_device), sel.to(cuda_device), mass=mass)
+    if q_scale <= 30:
+        check_rows(c, out, mass, [(i, 0, pos[i], sel[i].tolist()) for i in range(n)], many=True)
+        return
+    assert torch.isfinite(mass).all() and abs(float(mass.sum() - c.mass.sum().to(cuda_device)) - n * H) < 1e-4 * float(mass.sum())
+    got, clear = out.float().cpu().double(), 0
+    for i, p in enumerate(pos):
+        blocks = [j for j in sel[i].tolist() if j >= 0]
+        pg = c.table[0, blocks].long()
+        see = (torch.tensor(blocks)[:, None] * BLOCK + torch.arange(BLOCK) <= p).reshape(-1)
+        kk, vv = ((ref.values(x[pg]) * s[pg].double()[:, :, None, None]).transpose(0, 1).reshape(H, -1, 128)[:, see] for x, s in ((c.k, c.ks), (c.v, c.vs)))
+        z = torch.einsum("htd,hd->ht", kk, c.q[i].double()) * scale
+        err = (kk.abs() * c.q[i].double().abs()[:, None]).sum(-1).amax(dim=1) * scale * 2.0 ** -18
+        top, at = z.topk(2, dim=1)
+        lead = top[:, 0] - top[:, 1] > 2 * err + 2 ** 10
+        want = vv[torch.arange(H), at[:, 0]]
+        assert torch.isfinite(got[i]).all()
+        assert ((got[i] - want).abs() <= want.abs() * 2.0 ** -8 + 1e-38)[lead].all()
+        clear += int(lead.sum())
+    assert clear > 0.9 * n * H
+
+
 def test_many_queries_wait_timeout_is_flagged_and_recovers(uocr, cuda_device):
     """The waits for the keys give up at once: every block is dropped and flagged, the copies are waited
     for before their shared memory goes, and the next call is whole."""
