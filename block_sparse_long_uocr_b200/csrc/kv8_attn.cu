@@ -172,8 +172,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
 
     // the selection, the query and the lengths are on their way before any of them is used
     const int32_t *my_sel = sel + (size_t)i * kSel + slot;
-    // -2: not known yet; a caller's slot below 0 is empty, whatever its value
-    int j = implicit_local ? -2 : max(ld_pinned(my_sel), -1);
+    int j = implicit_local ? -2 : ld_pinned(my_sel);   // with implicit_local, -2: not known yet
     const uint2 raw = __ldg(q + (size_t)ih * (kD / 4) + lane);
     QueryRef r;
     const bool report = threadIdx.x == 0 && h == 0 && rank == 0;
@@ -182,7 +181,7 @@ sparse_attn_kv8_kernel(const uint2 *__restrict__ q, const uint4 *__restrict__ kc
         if (report) flag_error(dev_err, UOCR_DEVERR_POS);
         ok = false;
     }
-    if (!ok) j = -1;
+    if (!ok || (!implicit_local && j < 0)) j = -1;   // a caller's slot below 0 is empty, whatever its value
     if (j == -2) {   // after the selection kernel: slots that do not depend on the scores (see sparse_attn.cu)
         if (r.nb <= kSel)
             j = slot < r.nb ? slot : -1;
