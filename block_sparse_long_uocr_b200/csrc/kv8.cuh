@@ -83,6 +83,18 @@ __device__ __forceinline__ float f16_row_scale(float amax, float &inverse) {
     return __uint_as_float((uint32_t)(127 + k) << 23);
 }
 
+// What the products of a row in units of `unit` and of a block with scale ks are multiplied by to
+// give scores: unit * ks * scale.  unit and ks meet first (unit is as small as the row is large);
+// a factor past fp32's range stays finite, so that a product of 0 is a score of 0.  A ks that is not
+// finite gives NaN, in every form of the attention.
+__device__ __forceinline__ float score_factor(float unit, float ks, float scale) {
+    constexpr float kMax = 3.4028235e38f;
+    const float f = unit * ks * scale;
+    if (fabsf(f) <= kMax) return f;
+    const float a = fminf(fmaxf(unit * ks, -kMax), kMax);
+    return fminf(fmaxf(a * scale, -kMax), kMax) + (ks - ks);
+}
+
 // 2^x to 2 units; 0 below 2^-126.
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
@@ -142,7 +154,7 @@ __device__ __forceinline__ Query8 split_query8(Query8Smem &sm, uint2 raw, int la
     return q;
 }
 
-// Scores of a K tile, in units of q.unit * scale: every lane of quad g gets those of tokens g, 8 + g,
+// Scores of a K tile, in units of score_factor(q.unit, ..): every lane of quad g gets those of tokens g, 8 + g,
 // 16 + g, 24 + g.
 __device__ __forceinline__ void scores8(float (&z)[4], const uint4 (&k)[8], const Query8 &q, int lane) {
     float d[2][4];

@@ -280,17 +280,13 @@ kv8_block_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constan
         // and a weight is 2^((s - max) fa): 1 at the maximum and at most 1 elsewhere, however large the
         // scores are.  (2^(s fa - ma) with the product kept exact is one instruction less, but its exponent
         // at the maximum is the rounding of ma: from scores of 2^27 on that leaves fp16's range.)
-        ks *= scale_log2;
-        if (ks < 0.f) {   // a negative scale
+        if ((ks < 0.f) != (scale_log2 < 0.f)) {
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) s[nt][e] = -s[nt][e];
-            ks = -ks;
         }
-        // (a factor past fp32's range stays finite, so that a score of 0 stays 0)
-        const float fa = fabsf(ua * ks) > 3.4028235e38f ? 3.4028235e38f : ua * ks;
-        const float fb = fabsf(ub * ks) > 3.4028235e38f ? 3.4028235e38f : ub * ks;
+        const float fa = fabsf(score_factor(ua, ks, scale_log2)), fb = fabsf(score_factor(ub, ks, scale_log2));
         const bool partly = near < kBlock;   // some query does not see the whole block
         auto hidden = [&](int nt, int e, int pos) { return t0 + 8 * nt + 4 * e + c > pos; };
         if (partly) {

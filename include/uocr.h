@@ -394,7 +394,9 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  *                                              16-byte aligned
  *   k_scale, v_scale   fp32  [P][H]            value = code * scale of its (page, head)
  * Queries, outputs and the indexer cache stay bf16.  The attention takes any
- * finite scale; the writer below makes powers of two.
+ * finite scale, negative ones and 0 too; the writer below makes powers of two.  A
+ * (page, head) with a k_scale that is not finite makes the rows that attend it NaN,
+ * one with such a v_scale makes them NaN or infinite; other rows are not touched.
  *
  * mass, fp32 [B][H][max_blocks], optional (NULL: not kept): running totals of
  * the attention weight that each block received, the input of

@@ -397,6 +397,79 @@ def test_any_negative_slot_is_empty(uocr, cuda_device, empty):
     check_rows(c, out, mass, [(i, i, lens[i] - 1, sel[i].tolist()) for i in range(2)])
 
 
+def every_form(uocr, dev, c, n, scale):
+    """The attention of case c's n queries (rows of sequence 0, in blocks of its tokens from the last one back) by every
+    form: yields name, output, totals, rows and whether it is the block by block one."""
+    total = c.lens[0]
+    pos = [total - 1 - 5 * (i % 40) for i in range(n)]
+    nb = -(-total // BLOCK)
+    assert nb <= 16
+    sel = torch.full((n, 16), -1, dtype=torch.int32)
+    for i, p in enumerate(pos):
+        sel[i, :p // BLOCK + 1] = torch.arange(p // BLOCK + 1)
+    q, k, v, ks, vs, bt, sl = c.gpu(dev)
+    qp, se, seq = torch.tensor(pos, dtype=torch.int32, device=dev), sel.to(dev), torch.zeros(n, dtype=torch.int32, device=dev)
+    rows = [(i, 0, pos[i], sel[i].tolist()) for i in range(n)]
+    yield "sparse", uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, se, seq, qp, scale=scale), None, rows, False
+    for m in (5, n):
+        mass = c.mass.to(dev)
+        yield f"seq {m}", uocr.sparse_attn_seq_kv8(q[:m], k, v, ks, vs, bt, sl, 0, qp[:m], se[:m], scale=scale, mass=mass), mass, rows[:m], m == n
+    mass = c.mass.to(dev)
+    yield "one", uocr.sparse_attn_kv8(q[:1], k, v, ks, vs, bt, sl, se[:1], scale=scale, mass=mass), mass, rows[:1], False
+    if scale is None or abs(scale - 128 ** -0.5) < 1e-9:
+        mass = c.mass.to(dev)
+        yield "dense", uocr.dense_decode_kv8(q[:1], k, v, ks, vs, bt, sl, mass=mass), mass, rows[:1], False
+
+
+@pytest.mark.parametrize("q_scale,k_factor,scale", [(1e37, 2.0 ** -124, 128 ** -0.5),    # the row's unit times a product leaves fp32
+                                                    (1e-34, 2.0 ** 112, 128 ** -0.5),
+                                                    (1.0, -1.0, 128 ** -0.5), (1.0, -2.0 ** -3, -0.3),
+                                                    (0.0, 2.0 ** 129, 128 ** -0.5),      # products of 0 under scales near fp32's end
+                                                    (0.0, -2.0 ** 129, 100.0), (0.0, 2.0 ** 120, -1e6),
+                                                    (1e-30, 2.0 ** 129, 2.0 ** -30),
+                                                    (1.0, 1.0, 0.0)])
+def test_any_finite_key_scale_in_every_form(uocr, cuda_device, q_scale, k_factor, scale):
+    c = Case([450], 10, seed=94, n_q=100, q_scale=q_scale)
+    c.ks = (c.ks.double() / c.ks.max() * 2.0 ** -4 * k_factor).float()     # largest: 2^-4 k_factor
+    assert torch.isfinite(c.ks).all()
+    for name, out, mass, rows, many in every_form(uocr, cuda_device, c, 100, scale):
+        check_rows(c, out, mass, rows, scale=scale, many=many)
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("q_scale", [0.0, 1.0])
+def test_a_scale_that_is_not_finite_stays_with_its_rows(uocr, cuda_device, bad, which, q_scale):
+    """Head 3 of block 12 has such a scale: the rows that attend it are not finite (NaN for K) in that head, and theirs
+    alone; the K scale's weights add nothing, the V scale's are those of a finite one."""
+    c = Case([450], 10, seed=95, n_q=100, q_scale=q_scale)
+    page = int(c.table[0, 12])
+    plain = c.ks.clone(), c.vs.clone()
+    for name, out, mass, rows, many in every_form(uocr, cuda_device, c, 100, None):
+        (c.ks if which == "k" else c.vs)[page, 3] = bad
+        again = dict((x[0], x) for x in every_form(uocr, cuda_device, c, 100, None))[name]
+        c.ks, c.vs = plain[0].clone(), plain[1].clone()
+        hit = torch.tensor([p // BLOCK >= 12 for _, _, p, _ in rows])
+        got = again[1].float().cpu()
+        assert torch.isnan(got[hit][:, 3]).all() if which == "k" else not torch.isfinite(got[hit][:, 3]).any(), name
+        same = torch.ones_like(got, dtype=torch.bool)
+        same[hit, 3] = False
+        assert torch.equal(got[same], out.float().cpu()[same]), name
+        if mass is not None:
+            if which == "v":
+                assert torch.equal(mass, again[2]), name
+            else:
+                heads = [h for h in range(10) if h != 3]
+                assert torch.equal(mass[:, heads], again[2][:, heads]) and torch.isfinite(again[2]).all(), name
+                rest = c.mass.clone()
+                clean = [(i, b, p, x) for i, b, p, x in rows if p // BLOCK < 12]
+                for i, b, p, x in clean:
+                    _, w, _, _, used = c.want(i, b, p, x, 128 ** -0.5)
+                    for y, j in enumerate(used):
+                        rest[b, 3, j] += w[3, y]
+                assert ((again[2][:, 3].cpu() - rest[:, 3]).abs() <= 1e-4 * rest[:, 3].abs() + 1e-30).all(), name
+
+
 @pytest.mark.parametrize("n", [5, 100])      # a query at a time; block by block
 @pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-3, 30.0, 1e7, 1e8, 1e9, 1e20])
 def test_many_queries_of_any_magnitude(uocr, cuda_device, n, q_scale):
