@@ -660,10 +660,30 @@ def _kv8_specs(k_cache, v_cache, k_scale, v_scale, P, H):
             (k_scale, "k_scale", _F32, (P, H)), (v_scale, "v_scale", _F32, (P, H)))
 
 
-def _space(workspace, nbytes, dev: int):
+def _empty(shape, dtype, dev: int, stream):
+    """Memory on device `dev` that a call on `stream` (None: the current one) writes.  It is allocated for that stream:
+    the allocator gives out memory whose last work is still queued on the stream that asks, which is safe in that
+    stream's order only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=torch.device("cuda", dev))
+
+
+def _output(given, shape, dtype, dev: int, stream):
+    """The caller's output, or a new one, which the caller may use on the current stream and drop."""
+    if given is not None:
+        return given
+    t = _empty(shape, dtype, dev, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _space(workspace, nbytes, dev: int, stream):
     """The caller's workspace, or a new one of nbytes() bytes on device `dev`."""
     if workspace is None:
-        return torch.empty(max(nbytes(), 1), dtype=_U8, device=torch.device("cuda", dev))
+        return _empty(max(nbytes(), 1), _U8, dev, stream)
     if not (workspace.dtype is _U8 and workspace.dim() == 1 and workspace.get_device() == dev
             and workspace.is_contiguous()):
         _refuse(dev, (workspace, "workspace", _U8, (None,)))
@@ -671,8 +691,8 @@ def _space(workspace, nbytes, dev: int):
 
 
 def _lend(stream, *tensors):
-    """For a call on a stream other than the current one, whose tensors were allocated here: their memory is not
-    given out again before that stream is done with it."""
+    """For a call on a stream other than the current one: the memory of tensors that were allocated for the current one
+    is not given out again before that stream is done with it."""
     if stream is not None:
         for t in tensors:
             t.record_stream(stream)
@@ -757,11 +777,11 @@ def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_
     return q_out, idx_q_out
 
 
-def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, per_seq, out, mass, dev_err):
+def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, per_seq, out, mass, dev_err, stream):
     """The checks that the attention entry points share; per_seq: q has a row per sequence.  Returns (device, n, H, P,
     B, max_blocks, out)."""
-    if out is None and isinstance(q, torch.Tensor):
-        out = torch.empty_like(q)
+    if out is None and isinstance(q, torch.Tensor) and q.is_cuda:
+        out = _output(None, q.shape, _BF16, q.get_device(), stream)
     try:
         dev = q.get_device()
         n, H, _ = q.shape
@@ -800,10 +820,9 @@ def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, per
     return dev, n, H, P, B, mb, out
 
 
-def _index_args(dev, idx_q, idx_k_cache, sel, n, P):
+def _index_args(dev, idx_q, idx_k_cache, sel, n, P, stream):
     """The indexer's tensors of a whole step, and the selection's output."""
-    if sel is None:
-        sel = torch.empty((n, N_SEL), dtype=_I32, device=torch.device("cuda", dev))
+    sel = _output(sel, (n, N_SEL), _I32, dev, stream)
     _refuse(dev, (_need(idx_q, "idx_q"), "idx_q", _BF16, (n, IDX_DIM)),
             (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)), (sel, "sel", _I32, (n, N_SEL)))
     return sel
@@ -814,7 +833,7 @@ def sparse_attn_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens
     """sparse_attn over the 8-bit cache: bf16 [n_q, H, 128].  mass [B, H, max_blocks] fp32 (one query per
     sequence, q_seq None): each selected block's attention weight is added to its total."""
     dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
-                                            mass, dev_err)
+                                            mass, dev_err, stream)
     _need(sel, "sel")
     if not (sel.dtype is _I32 and sel.shape == (n_q, N_SEL) and sel.get_device() == dev and sel.is_contiguous()
             and q_seq is None and q_pos is None):
@@ -833,9 +852,9 @@ def sparse_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache,
                       sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_decode over the 8-bit cache.  Returns (out [B,H,128] bf16, sel [B,16] int32)."""
     dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, True, out,
-                                          mass, dev_err)
-    sel = _index_args(dev, idx_q, idx_k_cache, sel, B, P)
-    workspace = _space(workspace, lambda: workspace_bytes(B, H, mb), dev)
+                                          mass, dev_err, stream)
+    sel = _index_args(dev, idx_q, idx_k_cache, sel, B, P, stream)
+    workspace = _space(workspace, lambda: workspace_bytes(B, H, mb), dev, stream)
     _launch(_lib().uocr_sparse_decode_kv8, "sparse_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), B, H, mb, P, out.data_ptr(), sel.data_ptr(), _at(mass),
@@ -850,8 +869,8 @@ def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     when ref_blocks is None.  Returns out [B,H,128] bf16; mass [B, H, max_blocks] receives every attended block's
     weight."""
     dev, B, H, P, _, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, True, out,
-                                          mass, dev_err)
-    workspace = _space(workspace, lambda: dense_kv8_workspace_bytes(B, H, mb), dev)
+                                          mass, dev_err, stream)
+    workspace = _space(workspace, lambda: dense_kv8_workspace_bytes(B, H, mb), dev, stream)
     _launch(_lib().uocr_dense_decode_kv8, "dense_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             mb if ref_blocks is None else int(ref_blocks), B, H, mb, P, out.data_ptr(), _at(mass),
@@ -866,9 +885,9 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     """sparse_attn_seq over the 8-bit cache: many queries of sequence `seq` over the given selection.  Returns out
     [n_q,H,128] bf16; row `seq` of mass [B, H, max_blocks] receives the queries' weights."""
     dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
-                                            mass, dev_err)
+                                            mass, dev_err, stream)
     _refuse(dev, (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)), (_need(sel, "sel"), "sel", _I32, (n_q, N_SEL)))
-    workspace = _space(workspace, lambda: sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), dev)
+    workspace = _space(workspace, lambda: sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), dev, stream)
     _launch(_lib().uocr_sparse_attn_seq_kv8, "sparse_attn_seq_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
             int(seq), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
@@ -881,10 +900,10 @@ def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache
                        q_pos, *, out=None, sel=None, mass=None, workspace=None, dev_err=None, stream=None):
     """sparse_prefill over the 8-bit cache.  Returns (out [n_q,H,128] bf16, sel [n_q,16] int32)."""
     dev, n_q, H, P, B, mb, out = _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, False, out,
-                                            mass, dev_err)
-    sel = _index_args(dev, idx_q, idx_k_cache, sel, n_q, P)
+                                            mass, dev_err, stream)
+    sel = _index_args(dev, idx_q, idx_k_cache, sel, n_q, P, stream)
     _refuse(dev, (_need(q_pos, "q_pos"), "q_pos", _I32, (n_q,)))
-    workspace = _space(workspace, lambda: prefill_kv8_workspace_bytes(n_q, H, mb), dev)
+    workspace = _space(workspace, lambda: prefill_kv8_workspace_bytes(n_q, H, mb), dev, stream)
     _launch(_lib().uocr_sparse_prefill_kv8, "sparse_prefill_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
             block_table.data_ptr(), seq_lens.data_ptr(), int(seq), q_pos.data_ptr(), n_q, B, H, mb, P, out.data_ptr(),
@@ -900,14 +919,15 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
     [B,H,max_blocks] fp32, new_table [B,max_blocks] int32, new_lens [B] int32, freed [B,max_blocks] int32 pages,
     n_freed [B] int32); the first three may be the inputs themselves."""
     try:
-        new_mass = torch.empty_like(mass) if new_mass is None else new_mass
-        new_table = torch.empty_like(block_table) if new_table is None else new_table
-        new_lens = torch.empty_like(seq_lens) if new_lens is None else new_lens
-        freed = torch.empty_like(block_table) if freed is None else freed
-        n_freed = torch.empty_like(seq_lens) if n_freed is None else n_freed
         dev = mass.get_device()
         B, H, mb = totals = mass.shape
         table, lens = (B, mb), (B,)
+        if dev >= 0:
+            new_mass = _output(new_mass, totals, _F32, dev, stream)
+            new_table = _output(new_table, table, _I32, dev, stream)
+            new_lens = _output(new_lens, lens, _I32, dev, stream)
+            freed = _output(freed, table, _I32, dev, stream)
+            n_freed = _output(n_freed, lens, _I32, dev, stream)
         good = (dev >= 0 and mass.dtype is _F32 and mass.is_contiguous()
                 and block_table.dtype is _I32 and block_table.shape == table and block_table.get_device() == dev
                 and block_table.is_contiguous()
@@ -933,7 +953,7 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
                 (freed, "freed", _I32, (B, mb)), (n_freed, "n_freed", _I32, (B,)))
     if dev_err is not None:
         _check_dev_err(dev_err, dev)
-    workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev)
+    workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev, stream)
     _launch(_lib().uocr_evict_blocks, "evict_blocks", dev, stream, mass.data_ptr(), block_table.data_ptr(),
             seq_lens.data_ptr(), B, H, mb, int(keep_blocks), int(n_sink), new_mass.data_ptr(), new_table.data_ptr(),
             new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), workspace.data_ptr(), workspace.numel(),

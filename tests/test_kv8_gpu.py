@@ -946,6 +946,60 @@ def test_memory_of_a_call_on_another_stream_is_not_given_out(uocr, cuda_device, 
     assert again.data_ptr() != at and other.data_ptr() != dropped
 
 
+def test_a_call_on_another_stream_takes_no_memory_with_work_queued_on_the_current_one(uocr, cuda_device):
+    """Tensors dropped while the current stream still has to read them: a call on another stream that allocates the same
+    sizes writes elsewhere.  And the other way round: an output dropped while the current stream still reads it."""
+    c = Case([2000], 10, seed=36)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    mass = c.mass.to(cuda_device)
+    g = torch.Generator().manual_seed(1)
+    iq, ik = (torch.randn(s, generator=g).to(torch.bfloat16).to(cuda_device) for s in ((1, 128), (k.shape[0], 32, 128)))
+    n = 100
+    qn, pos = q.expand(n, -1, -1).contiguous(), torch.arange(1900, 2000, dtype=torch.int32, device=cuda_device)
+    sel = c.select([1999] * n)
+    sel = torch.where(sel > pos.cpu()[:, None] // BLOCK, -1, sel).to(cuda_device)
+    iqn = iq.expand(n, -1).contiguous()
+    calls = {
+        "sparse": (lambda s: (uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, sel[:1], stream=s),), 0),
+        "decode": (lambda s: uocr.sparse_decode_kv8(q, k, v, ks, vs, iq, ik, bt, sl, stream=s), uocr.workspace_bytes(1, 10, c.mb)),
+        "dense": (lambda s: (uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, stream=s),), uocr.dense_kv8_workspace_bytes(1, 10, c.mb)),
+        "seq": (lambda s: (uocr.sparse_attn_seq_kv8(qn, k, v, ks, vs, bt, sl, 0, pos, sel, stream=s),), uocr.sparse_attn_seq_kv8_workspace_bytes(n, 10, c.mb)),
+        "prefill": (lambda s: uocr.sparse_prefill_kv8(qn, k, v, ks, vs, iqn, ik, bt, sl, 0, pos, stream=s), uocr.prefill_kv8_workspace_bytes(n, 10, c.mb)),
+        "evict": (lambda s: uocr.evict_blocks(mass, bt, sl, 20, stream=s), uocr.evict_workspace_bytes(1, 10, c.mb)),
+    }
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for name, (call, space) in calls.items():
+        want = [x.clone() for x in call(None)]
+        torch.cuda.synchronize()
+        sizes = [x.numel() * x.element_size() for x in want] + [space] * (space > 0)
+        torch.cuda.empty_cache()
+        temps = [torch.full((x,), 0x5A, dtype=torch.uint8, device=cuda_device) for x in sizes]
+        keep = [torch.zeros_like(t) for t in temps]
+        torch.cuda.synchronize()
+        torch.cuda._sleep(20_000_000)
+        for a, b in zip(keep, temps):
+            a.copy_(b)
+        del temps, a, b
+        got = call(side)
+        side.synchronize()
+        busy = not torch.cuda.current_stream().query()
+        assert busy, "the current stream was done before the call on the other"
+        torch.cuda.synchronize()
+        assert all((x == 0x5A).all() for x in keep), name
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), name
+        torch.cuda._sleep(20_000_000)
+        later = [x.clone() for x in got]
+        del got
+        other = call(side)          # must not be given the memory that the clones still have to read
+        for x in other:
+            with torch.cuda.stream(side):
+                x.zero_()
+        side.synchronize()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(later, want)), name
+
+
 def test_prompt_decode_evict_decode(uocr, cuda_device):
     """The operators as a server uses them: a prompt appended and attended in two chunks, decode steps, an eviction in
     place, pages freed, more decode steps on the shorter table; every attention against the 64-bit form on the cache
