@@ -16,7 +16,9 @@
 // x is the rotated key in 64 bits (angles, sines; products in 64 bits or as sums of two fp32
 // numbers) rounded once, to nearest even: on its way through 32 bits it is rounded to odd, which no
 // later rounding to fewer bits can see.  So
-// a code is a function of its inputs' exact values, the same whatever chunk its token came in.
+// a code is a function of its inputs' exact values, the same whatever chunk its token came in.  The
+// rotated queries and indexer vectors are rounded once to bf16 in the same way, so that neither
+// they nor the blocks that they select depend on the chunk.
 // Infinities and NaN are stored as e4m3's NaN (it has no infinity, and a saturated one would look
 // like a value).
 //
@@ -27,8 +29,9 @@
 //   many: CTA (run, a few heads), thread (token, 8 pairs) of 32 tokens: the sines of a page are
 //       formed once for the CTA's heads and kept in registers, every load and store is 8 or 16 bytes.
 //       2048 tokens, 10 heads: 27.7 us with the first kernel (11 times the sines, 64-bit conversions
-//       at 16 a clock), 14.5 here: bound by the issue of the rotation's two-number products (about
-//       900 instructions a thread and head) and one barrier a head, not by its 28 MB (4.3 us).
+//       at 16 a clock), 15.4 here: bound by the issue of the rotation's two-number products (about
+//       1000 instructions a thread and head) and one barrier a head, not by its 28 MB (4.3 us).  1.4 of
+//       them are what the queries' single rounding costs (a test of each value in fp32).
 #include <math.h>
 
 #include "kernels.h"
@@ -45,6 +48,13 @@ constexpr int kMinExp = -126;   // the least scale: 2^-126, the smallest normal 
 __device__ __forceinline__ float round_odd(double x) {
     const float t = __double2float_rz(x);
     return (double)t != x && isfinite(t) ? __uint_as_float(__float_as_uint(t) | 1u) : t;
+}
+
+// Pair (x0, x1) turned by an angle, in 64 bits.  (Spelled out, so that every kernel's products and sums
+// are rounded alike.)
+__device__ __forceinline__ void turn(double x0, double x1, double cs, double sn, double &r0, double &r1) {
+    r0 = fma(x0, cs, -__dmul_rn(x1, sn));
+    r1 = fma(x1, cs, __dmul_rn(x0, sn));
 }
 
 // Exponent e of the least power of two with 2 half <= 448 * 2^e, at least kMinExp.  half >= 0, finite.
@@ -161,13 +171,12 @@ rope_append_kv8_few_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, c
         sincos(coord * freqs.inv[pair], &sn, &cs);
         const __nv_bfloat16 *src = h < H ? q + ((size_t)i * H + h) * kD : idx_q + (size_t)i * kDIdx;
         __nv_bfloat16 *dst = h < H ? q_out + ((size_t)i * H + h) * kD : idx_q_out + (size_t)i * kDIdx;
-        double x0 = (double)__bfloat162float(src[pair]), x1 = (double)__bfloat162float(src[pair + kPairs]);
-        dst[pair] = __float2bfloat16_rn(round_odd(x0 * cs - x1 * sn));
-        dst[pair + kPairs] = __float2bfloat16_rn(round_odd(x1 * cs + x0 * sn));
+        double r0, r1;
+        turn((double)__bfloat162float(src[pair]), (double)__bfloat162float(src[pair + kPairs]), cs, sn, r0, r1);
+        dst[pair] = __float2bfloat16_rn(round_odd(r0));
+        dst[pair + kPairs] = __float2bfloat16_rn(round_odd(r1));
         src = h < H ? k_new + ((size_t)i * H + h) * kD : idx_k_new + (size_t)i * kDIdx;
-        x0 = (double)__bfloat162float(src[pair]);
-        x1 = (double)__bfloat162float(src[pair + kPairs]);
-        const double r0 = x0 * cs - x1 * sn, r1 = x1 * cs + x0 * sn;
+        turn((double)__bfloat162float(src[pair]), (double)__bfloat162float(src[pair + kPairs]), cs, sn, r0, r1);
         if (h < H) {
             const float y0 = round_odd(0.5 * r0), y1 = round_odd(0.5 * r1);
             s_x[t][pair] = y0;
@@ -218,26 +227,24 @@ rope_append_kv8_few_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, c
 namespace {
 constexpr int kManyThreads = kBlock * kPairs / 8;   // thread (token, 8 pairs)
 
-// hi + lo, |lo| at most half a unit of hi, rounded to odd.
+// hi + lo, rounded to odd.
 __device__ __forceinline__ float round_odd(float hi, float lo) {
     if (lo == 0.f) return hi;   // (keeps the sign of a zero)
     const float s = __fadd_rz(hi, lo);
     return (hi - s) + lo != 0.f && isfinite(s) ? __uint_as_float(__float_as_uint(s) | 1u) : s;
 }
 
-// a x + b y to about 2^-46 of its terms, rounded to odd; a and b as sums of two fp32 numbers.
+// a x + b y to about 2^-46 of its terms, rounded to odd; a and b as sums of two fp32 numbers.  Products
+// with their rounding errors by fma, the sum with its own by Knuth's TwoSum, and an odd rounding (Boldo and
+// Melquiond: a later rounding to fewer bits then is the only one).  Written with the functions that are
+// never joined: made one fma, p + q is no longer the sum of the two whose errors are added below, and the
+// result is off by 2^-25.
 __device__ __forceinline__ float dot2_odd(float x, float ah, float al, float y, float bh, float bl) {
-    const float p = x * ah, pe = fmaf(x, ah, -p);
-    const float q = y * bh, qe = fmaf(y, bh, -q);
-    const float s = p + q, t = s - p;
-    const float e = (p - (s - t)) + (q - t);
-    return round_odd(s, fmaf(x, al, fmaf(y, bl, e + (pe + qe))));
-}
-
-// a x + b y to fp32, also where the terms cancel: the products' errors and the low parts added.
-__device__ __forceinline__ float dot2(float x, float ah, float al, float y, float bh, float bl) {
-    const float q = y * bh;
-    return fmaf(x, ah, q) + (fmaf(y, bh, -q) + fmaf(x, al, y * bl));
+    const float p = __fmul_rn(x, ah), pe = fmaf(x, ah, -p);
+    const float q = __fmul_rn(y, bh), qe = fmaf(y, bh, -q);
+    const float s = __fadd_rn(p, q), t = __fsub_rn(s, p);
+    const float e = __fadd_rn(__fsub_rn(p, __fsub_rn(s, t)), __fsub_rn(q, t));
+    return round_odd(s, fmaf(x, al, fmaf(y, bl, __fadd_rn(e, __fadd_rn(pe, qe)))));
 }
 
 // Eight numbers (times inv) to packed codes; what is not finite to NaN.
@@ -269,6 +276,29 @@ __device__ __forceinline__ uint4 rescale_e4m3(uint4 v, float ratio) {
     return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
+// Whether 64 bits that are off by up to `off` round to bf16 as their exact value does: they are not that
+// near a midpoint.  False for what is below bf16's normal range or not finite.
+__device__ __forceinline__ bool decided(double r, double off) {
+    const double a = fabs(r);
+    const long long midpoint = (__double_as_longlong(a) & ~((1ll << 45) - 1)) | 1ll << 44;
+    return a >= 0x1p-126 && fabs(a - __longlong_as_double(midpoint)) > off;
+}
+
+// A pair turned and rounded to odd, as the few-token kernel does.  The sum of the two fp32 numbers that
+// stand for a sine is off by 2^-49, which nearly always decides the rounding; else the sine is formed again.
+__device__ __noinline__ float2 turn_exactly(float x0, float x1, float ch, float cl, float sh, float sl, int coord,
+                                            double inv) {
+    double r0, r1;
+    turn((double)x0, (double)x1, (double)ch + (double)cl, (double)sh + (double)sl, r0, r1);
+    const double off = (fabs((double)x0) + fabs((double)x1)) * 0x1p-44;
+    if (!decided(r0, off) || !decided(r1, off)) {
+        double sn, cs;
+        sincos((double)coord * inv, &sn, &cs);
+        turn((double)x0, (double)x1, cs, sn, r0, r1);
+    }
+    return make_float2(round_odd(r0), round_odd(r1));
+}
+
 __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
     uint32_t r[4];
 #pragma unroll
@@ -280,7 +310,7 @@ __device__ __forceinline__ uint4 pack_bf16x8(const float (&x)[8]) {
 }
 }  // namespace
 
-__global__ void __launch_bounds__(kManyThreads)
+__global__ void __launch_bounds__(kManyThreads, 2)
 rope_append_kv8_many_kernel(const uint4 *q, const uint4 *idx_q, const uint4 *__restrict__ k_new,
                             const uint4 *__restrict__ v_new, const uint4 *__restrict__ idx_k_new,
                             const int32_t *__restrict__ tok_pos, const int32_t *__restrict__ page_pos,
@@ -303,22 +333,47 @@ rope_append_kv8_many_kernel(const uint4 *q, const uint4 *idx_q, const uint4 *__r
     }
     const bool mine = t < run.count;
     const int i = run.first + (mine ? t : 0);
+    auto coord = [&](int pair) {
+        return pair < kPairs - UOCR_ROPE_PAGE_PAIRS ? __ldg(tok_pos + i) : ((__ldg(page_pos + i) % 2) + 2) % 2;
+    };
     // cosines and sines of the thread's pairs, as sums of two fp32 numbers
     float ch[8], cl[8], sh[8], sl[8];
     if (mine) {
-        const int page_mod2 = ((__ldg(page_pos + i) % 2) + 2) % 2;
-        const double tok = (double)__ldg(tok_pos + i);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const int pair = 8 * c + e;
             double sn, cs;
-            sincos((pair < kPairs - UOCR_ROPE_PAGE_PAIRS ? tok : (double)page_mod2) * freqs.inv[pair], &sn, &cs);
+            sincos((double)coord(8 * c + e) * freqs.inv[8 * c + e], &sn, &cs);
             ch[e] = (float)cs;
             cl[e] = (float)(cs - (double)ch[e]);
             sh[e] = (float)sn;
             sl[e] = (float)(sn - (double)sh[e]);
         }
     }
+    // Eight pairs to bf16, rounded once from their value in 64 bits as in the few-token kernel.  In fp32
+    // a value is off by at most 2.5 * 2^-24 of its terms (a product's rounding, the sum's, half a unit of
+    // each sine); only where that could take it over a midpoint of bf16 (some 2^-11 of all values), or a term
+    // is not finite, is its pair turned in 64 bits.
+    auto rotate_bf16 = [&](const uint4 (&in)[2], uint4 &low, uint4 &high) {
+        float x0[8], x1[8], o0[8], o1[8];
+        bf16x8_to_f32(in[0], x0);
+        bf16x8_to_f32(in[1], x1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            o0[e] = fmaf(x0[e], ch[e], -x1[e] * sh[e]);
+            o1[e] = fmaf(x1[e], ch[e], x0[e] * sh[e]);
+            const float off = fmaf(fabsf(x0[e]) + fabsf(x1[e]), 0x1.8p-23f, 0x1p-146f);   // (fp32's least values too)
+            auto far = [&](float o) {   // from the midpoint of its bf16 neighbours; false for NaN
+                return fabsf(o - __uint_as_float((__float_as_uint(o) & 0xffff0000u) | 0x8000u)) > off;
+            };
+            if (!far(o0[e]) || !far(o1[e])) {
+                const float2 o = turn_exactly(x0[e], x1[e], ch[e], cl[e], sh[e], sl[e], coord(8 * c + e), freqs.inv[8 * c + e]);
+                o0[e] = o.x;
+                o1[e] = o.y;
+            }
+        }
+        low = pack_bf16x8(o0);
+        high = pack_bf16x8(o1);
+    };
 
     for (int h = h0; h < h1; ++h) {
         const bool idx = h == H;
@@ -344,31 +399,22 @@ rope_append_kv8_many_kernel(const uint4 *q, const uint4 *idx_q, const uint4 *__r
         float y[16], v[16];   // half of the rotated key (dims 8 c .. and 64 + 8 c ..), half of the values
         float2 top = make_float2(0.f, 0.f);
         if (mine) {
-            float x0[8], x1[8], o0[8], o1[8];
-            bf16x8_to_f32(qv[0], x0);
-            bf16x8_to_f32(qv[1], x1);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                o0[e] = dot2(x0[e], ch[e], cl[e], -x1[e], sh[e], sl[e]);
-                o1[e] = dot2(x1[e], ch[e], cl[e], x0[e], sh[e], sl[e]);
-            }
+            uint4 low, high;
+            rotate_bf16(qv, low, high);
             uint4 *dst = idx ? idx_q_out : q_out;
-            dst[row + c] = pack_bf16x8(o0);
-            dst[row + 8 + c] = pack_bf16x8(o1);
-            bf16x8_to_f32(kv[0], x0);
-            bf16x8_to_f32(kv[1], x1);
+            dst[row + c] = low;
+            dst[row + 8 + c] = high;
             if (idx) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    o0[e] = dot2(x0[e], ch[e], cl[e], -x1[e], sh[e], sl[e]);
-                    o1[e] = dot2(x1[e], ch[e], cl[e], x0[e], sh[e], sl[e]);
-                }
+                rotate_bf16(kv, low, high);
                 if (page >= 0) {
                     uint4 *to = idx_k_cache + ((size_t)page * kBlock + run.row + t) * (kDIdx / 8);
-                    to[c] = pack_bf16x8(o0);
-                    to[8 + c] = pack_bf16x8(o1);
+                    to[c] = low;
+                    to[8 + c] = high;
                 }
             } else {
+                float x0[8], x1[8];
+                bf16x8_to_f32(kv[0], x0);
+                bf16x8_to_f32(kv[1], x1);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float a = 0.5f * x0[e], b = 0.5f * x1[e];

@@ -428,9 +428,10 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  *   s = need, if the page holds no older row of the sequence, else
  *       max(s_old rounded up to a power of two, need);
  * a new value x is stored as e4m3(x / s), and where s != s_old the older rows'
- * codes c become e4m3(c * s_old / s), s_old finite.  Rounding is to nearest even,
- * once, from the value in 64 bits; infinities and NaN are stored as NaN.  Rows of the
- * page behind the sequence's end keep what they hold.
+ * codes c become e4m3(c * s_old / s), s_old finite.  Rounding, of codes and of the
+ * rotated bf16 vectors alike, is to nearest even, once, from the value in 64 bits,
+ * whatever the number of tokens; infinities and NaN are stored as the codes of NaN.
+ * Rows of the page behind the sequence's end keep what they hold.
  * A page must not receive tokens from two sequences in one call.  A sequence
  * whose new_start is not as above, with more new tokens than seq_lens, or
  * longer than its table is skipped (its q rows too) and sets UOCR_DEVERR_POS; a

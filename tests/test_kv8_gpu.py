@@ -632,6 +632,77 @@ def test_append_is_the_same_in_any_chunks(uocr, cuda_device):
     assert torch.equal(whole["idx_k"], d["idx_k"].cpu())
 
 
+def bf16_rounded(x):
+    """64-bit values to the nearest bf16 (ties to even, past the last one to infinity), and how far each is from a
+    midpoint."""
+    x = np.asarray(x, dtype=np.float64)
+    fine = np.isfinite(x)
+    a = np.where(fine, np.abs(x), 0.0)
+    step = np.ldexp(1.0, np.maximum(np.frexp(a)[1] - 8, -133))
+    y = np.rint(a / step) * step
+    gap = np.abs(np.abs(a / step - np.floor(a / step)) - 0.5) * step
+    y = np.where(y > 3.3895314e38, np.inf, y)
+    return np.where(fine, np.copysign(y, x), x), gap
+
+
+def test_append_rounds_once_in_both_kernels(uocr, cuda_device):
+    """The same tokens as 6 a sequence (the kernel for few) and beside a longer sequence (the one for many): equal
+    queries, indexer vectors, codes and scales, and each the 64-bit rotation rounded once to bf16."""
+    H, B = 10, 160
+    lens, new = [6 + (5 * b) % 70 for b in range(B)] + [40], [6] * B + [40]
+    s, table, starts, n = append_state(80, H, lens, new)
+    few = {x: (v[:6 * B] if v.shape[0] == n else v) for x, v in s.items()}
+    got = [run_append(uocr, cuda_device, few, table[:B], lens[:B], starts[:B + 1]), run_append(uocr, cuda_device, s, table, lens, starts)]
+    pages = sorted({int(p) for b in range(B) for p in table[b] if p >= 0})
+    assert torch.equal(got[0][0], got[1][0][:6 * B]) and torch.equal(got[0][1], got[1][1][:6 * B])
+    for x in got[0][2]:
+        assert torch.equal(got[0][2][x].view(torch.uint8)[pages], got[1][2][x].view(torch.uint8)[pages]), x
+    tok, page = s["tok"].numpy(), s["page"].numpy()
+    ang = np.concatenate([tok[:, None].astype(np.float64) * np.array([10000.0 ** (-j / 63) for j in range(63)]), (page % 2)[:, None]], axis=1)
+    c, sn = np.cos(ang), np.sin(ang)
+    for src, out, cc, ss in ((s["q"], got[1][0], c[:, None], sn[:, None]), (s["idx_q"], got[1][1], c, sn)):
+        x = src.double().numpy()
+        a, b = x[..., :64], x[..., 64:]
+        w = np.concatenate([a * cc - b * ss, b * cc + a * ss], axis=-1)
+        want, gap = bf16_rounded(w)
+        # the reference's angles and products are themselves off by a few 2^-53 of 120000 rad and of the terms
+        sure = gap > 2.0 ** -34 * np.concatenate([np.abs(a) + np.abs(b)] * 2, axis=-1)
+        assert sure.mean() > 0.9999
+        assert (out.double().cpu().numpy() == want)[sure].all()
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf, math.nan, 3.3e38, -3.3e38, 0.0, 1e-38, -3e-40, 1e-30])
+def test_append_extreme_values_alike_in_both_kernels(uocr, cuda_device, value):
+    """Infinities, NaN, the largest and the smallest numbers in either half of q, idx_q, k, idx_k and v, at position 0 too (a sine
+    of 0): the kernel for few tokens and the one for many give the same, NaN where the other has NaN."""
+    H, B = 2, 12
+    lens, new = [6 + 3 * b for b in range(B)] + [60], [6] * B + [60]
+    s, table, starts, n = append_state(81, H, lens, new)
+    s["tok"][::4] = 0
+    s["page"][::3] = 0
+    for name in ("q", "k_new", "v_new", "idx_q", "idx_k_new"):
+        x = s[name].view(n, -1, 128)
+        x[1::6, :, 3] = value              # first half, second half, both, whole rows
+        x[2::6, :, 67] = value
+        x[3::6, :, 5], x[3::6, :, 69] = value, -value
+        x[4::6] = value
+        x[::4, :, 63], x[1::4, :, 127] = value, value      # the page's pair
+    few = {x: (v[:6 * B] if v.shape[0] == n else v) for x, v in s.items()}
+    a = run_append(uocr, cuda_device, few, table[:B], lens[:B], starts[:B + 1])
+    b = run_append(uocr, cuda_device, s, table, lens, starts)
+    pages = sorted({int(p) for x in range(B) for p in table[x] if p >= 0})
+
+    def alike(x, y):
+        x, y = x.float(), y.float()
+        return bool(((x == y) | (torch.isnan(x) & torch.isnan(y))).all())
+
+    assert alike(a[0], b[0][:6 * B]) and alike(a[1], b[1][:6 * B])
+    for x in a[2]:
+        assert alike(a[2][x][pages], b[2][x][pages]), x
+    if not math.isfinite(value):
+        assert torch.isinf(a[0].float()).any() == math.isinf(value)
+
+
 def test_append_extreme_values(uocr, cuda_device):
     lens, H = [40, 64], 2
     s, table, starts, n = append_state(6, H, lens, [20, 64])
@@ -648,6 +719,32 @@ def test_append_extreme_values(uocr, cuda_device):
     want = ref.append(s, starts, lens, table)
     got = run_append(uocr, cuda_device, s, table, lens, starts)
     check_append(s, got, want, (torch.full_like(s["q"], 7.0), torch.full_like(s["idx_q"], 7.0)))
+
+
+def test_append_codes_alike_in_both_kernels_over_many_values(uocr, cuda_device):
+    """30 million keys as 6 a sequence (the kernel for few) and beside a longer sequence (the one for many): a sum that
+    is off by 2^-25 of its terms would give another code for some ten of them."""
+    H, B, dev = 16, 2500, cuda_device
+    g = torch.Generator(device=dev).manual_seed(82)
+    n = 6 * B + 40
+    rnd = lambda *shape: torch.randn(shape, generator=g, device=dev).to(torch.bfloat16)  # noqa: E731
+    q, k, v, iq, ik = rnd(n, H, 128), rnd(n, H, 128), rnd(n, H, 128), rnd(n, 128), rnd(n, 128)
+    tok = torch.randint(0, 100000, (n,), generator=g, device=dev, dtype=torch.int32)
+    table = torch.arange(2 * (B + 1), device=dev, dtype=torch.int32).reshape(B + 1, 2)
+    lens = torch.tensor([6] * B + [40], device=dev, dtype=torch.int32)
+    starts = torch.tensor([6 * b for b in range(B + 1)] + [n], device=dev, dtype=torch.int32)
+    P, got = 2 * (B + 1), []
+    for b in (B, B + 1):
+        m = int(starts[b])
+        c = [torch.zeros((P, H, 32, 128), dtype=torch.uint8, device=dev).view(torch.float8_e4m3fn) for _ in range(2)]
+        s = [torch.zeros((P, H), device=dev) for _ in range(2)]
+        cik = torch.zeros((P, 32, 128), dtype=torch.bfloat16, device=dev)
+        uocr.rope_append_kv8(q[:m], iq[:m], k[:m], v[:m], ik[:m], tok[:m], tok[:m], table[:b], lens[:b], *c, *s, cik, starts[:b + 1],
+                             q_out=torch.empty_like(q[:m]), idx_q_out=torch.empty_like(iq[:m]))
+        got.append([x.view(torch.uint8)[:2 * B] for x in (*c, *s)])
+    assert int((got[0][0] & 0x7F).max()) > 100
+    for a, b in zip(*got):
+        assert torch.equal(a, b), int((a != b).sum())
 
 
 def test_append_bad_sequences_are_skipped(uocr, cuda_device):
