@@ -559,8 +559,8 @@ namespace {
 // sequences' fit on the SMs at once, and more where only a smaller slice fits in shared memory; 0
 // where none does.  Measured at 64 sequences of 4096 blocks and at 3 of 777, 10 to 12 heads (us):
 // 1 CTA 23.8 / 8.5, 2: 18.0 / 7.8, 4: 26.5 / 7.6; the three-launch form 30.5 / 13.8.
+constexpr size_t kRoom = 192 * 1024;   // shared memory of the slice and the keys
 int evict_ctas(int B, int H, int max_blocks, int num_sms) {
-    constexpr size_t kRoom = 192 * 1024;
     int ctas = 4;
     while (ctas > 1 && (long long)B * ctas > num_sms && one_smem(H, max_blocks, ctas / 2) <= kRoom) ctas /= 2;
     while (ctas < kMaxCluster && one_smem(H, max_blocks, ctas) > kRoom) ctas *= 2;
@@ -585,7 +585,8 @@ cudaError_t launch_evict(const LaunchCtx &c, const float *mass, const int32_t *t
     const int ctas = evict_ctas(B, H, max_blocks, c.num_sms);
     if (ctas > 0) {
         const size_t smem = one_smem(H, max_blocks, ctas);
-        cudaError_t e = cudaFuncSetAttribute(evict_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        // the same for every call: another thread's call for a smaller table must not lower it before this launch
+        cudaError_t e = cudaFuncSetAttribute(evict_one_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRoom);
         if (e != cudaSuccess) return e;
         const int wide = max_blocks % 4 == 0 && ((uintptr_t)mass | (uintptr_t)table) % 16 == 0;
         const int wide_out = max_blocks % 4 == 0 && ((uintptr_t)new_mass | (uintptr_t)new_table) % 16 == 0;

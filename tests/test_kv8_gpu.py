@@ -840,6 +840,44 @@ def test_evict_on_the_largest_clusters(uocr, cuda_device, mb, H):
             assert torch.equal(w, x), (name, keep, sink)
 
 
+def test_evict_from_several_threads(uocr, cuda_device):
+    """Tables of very different widths (shared memory from 9 to 190 KiB a CTA) evicted by threads of their own, each on
+    its stream: every call is launched and gives what it gives alone."""
+    import threading
+    g = torch.Generator().manual_seed(60)
+    jobs = []
+    for mb, H in ((40, 1), (12000, 10), (700, 64), (40, 2)):
+        mass = torch.exp(2 * torch.randn((2, H, mb), generator=g)).to(cuda_device)
+        table = torch.randint(0, 1 << 20, (2, mb), generator=g, dtype=torch.int32).to(cuda_device)
+        lens = torch.tensor([mb * BLOCK, mb * BLOCK - 40], dtype=torch.int32, device=cuda_device)
+        want = [x.clone() for x in uocr.evict_blocks(mass, table, lens, mb // 2, n_sink=1)]
+        jobs.append((mass, table, lens, mb // 2, want))
+    torch.cuda.synchronize()
+    wrong, ready = [], threading.Barrier(2 * len(jobs))
+
+    def work(job):
+        mass, table, lens, keep, want = job
+        (B, H, mb), out = mass.shape, [torch.empty_like(x) for x in want]
+        ws = torch.empty(uocr.evict_workspace_bytes(B, H, mb), dtype=torch.uint8, device=cuda_device)
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        at = [x.data_ptr() for x in out]
+        args = (mass.data_ptr(), table.data_ptr(), lens.data_ptr(), B, H, mb, keep, 1, *at, ws.data_ptr(), ws.numel(), None, stream.cuda_stream)
+        call = uocr.lib.uocr_evict_blocks      # as the binding calls it, without its checks, so that the threads meet
+        ready.wait()
+        bad = sum(call(*args) != 0 for _ in range(3000))
+        stream.synchronize()
+        if bad or not all(torch.equal(a, b) for a, b in zip(want, out)):
+            wrong.append((mb, H, bad))
+
+    threads = [threading.Thread(target=work, args=(job,)) for job in jobs + jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
+
+
 def test_evict_bad_lengths_copy_and_flag(uocr, cuda_device):
     mass, table = torch.rand((3, 2, 50)), torch.arange(150, dtype=torch.int32).reshape(3, 50)
     lens = torch.tensor([-1, 50 * BLOCK + 1, 1000], dtype=torch.int32)
