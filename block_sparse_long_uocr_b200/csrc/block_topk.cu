@@ -111,9 +111,10 @@ cudaError_t launch_block_topk(const LaunchCtx &c, const float *scores, const int
     const int staged = max_blocks <= kTopkSmemKeys;
     const size_t smem = staged ? (size_t)max_blocks * sizeof(uint32_t) : 0;
     if (smem > 16 * 1024) {
-        // the static shared memory (~18 KiB) plus the staged keys may pass the 48 KiB default
+        // the static shared memory (~18 KiB) plus the staged keys may pass the 48 KiB default; the limit is
+        // the same for every call: another thread's call for shorter rows must not lower it before this launch
         cudaError_t e = cudaFuncSetAttribute(block_topk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+                                             kTopkSmemKeys * (int)sizeof(uint32_t));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

@@ -840,6 +840,48 @@ def test_evict_on_the_largest_clusters(uocr, cuda_device, mb, H):
             assert torch.equal(w, x), (name, keep, sink)
 
 
+def meet(calls, times):
+    """Each call's arguments, times over from two threads of its own, all at once; the numbers of failed ones.  As the
+    binding calls the library, without its checks, so that the threads meet."""
+    import threading
+    failed, ready = [], threading.Barrier(2 * len(calls))
+
+    def work(call, args):
+        stream = torch.cuda.Stream()
+        stream.wait_stream(torch.cuda.current_stream())
+        args = args()
+        ready.wait()
+        failed.append(sum(call(*args, stream.cuda_stream) != 0 for _ in range(times)))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=x) for x in calls + calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    return failed
+
+
+def test_selection_from_several_threads(uocr, cuda_device):
+    """Rows of very different widths (staged in 18 to 120 KiB of shared memory) by threads of their own: every call is
+    launched and gives what it gives alone."""
+    g = torch.Generator().manual_seed(61)
+    calls, outs = [], []
+    for mb in (4400, 30000, 17000):
+        scores = torch.randn((3, mb), generator=g).to(cuda_device)
+        lens = torch.tensor([mb * BLOCK, mb * BLOCK - 40, 5000], dtype=torch.int32, device=cuda_device)
+        want = uocr.block_topk(scores, lens)
+
+        def args(scores=scores, lens=lens, mb=mb, want=want):
+            outs.append((torch.empty_like(want), want, scores, lens))
+            return scores.data_ptr(), lens.data_ptr(), None, None, 3, 3, mb, outs[-1][0].data_ptr(), None
+
+        calls.append((uocr.lib.uocr_block_topk, args))
+    torch.cuda.synchronize()
+    assert meet(calls, 3000) == [0] * 6
+    assert len(outs) == 6 and all(torch.equal(a, b) for a, b, *_ in outs)
+
+
 def test_evict_from_several_threads(uocr, cuda_device):
     """Tables of very different widths (shared memory from 9 to 190 KiB a CTA) evicted by threads of their own, each on
     its stream: every call is launched and gives what it gives alone."""
