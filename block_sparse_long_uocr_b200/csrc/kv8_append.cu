@@ -7,7 +7,7 @@
 // adds to a (page, head), separately for K and V:
 //   need = 2^max(ceil(log2(amax / 448)), -126),  amax over the rows' finite values;
 //   s    = need when the page holds no older row of the sequence,
-//          max(s_old rounded up to a power of two, need) otherwise;
+//          max(|s_old| rounded up to a power of two, need) otherwise;
 //   new code = e4m3(x / s), older code c -> e4m3(c s_old / s).
 // A scale is a power of two, so that dividing by it is exact, and raising it moves the older codes'
 // exponents: they are rounded again only where they fall below e4m3's normal range.  It only
@@ -65,10 +65,11 @@ __device__ __forceinline__ int scale_exp(float half) {
     return max(kMinExp, (b & 0x7fffffu) <= 0x600000u ? e - 7 : e - 6);
 }
 
-// A stored scale rounded up to a power of two: its exponent, in [kMinExp, 127].
+// A stored scale's magnitude rounded up to a power of two: its exponent, in [kMinExp, 127].  (A negative
+// scale turns its codes' signs when they are rescaled.)
 __device__ __forceinline__ int scale_exp_of(float s) {
-    const uint32_t b = __float_as_uint(s);
-    if (!(s >= 1.17549435e-38f)) return kMinExp;   // not positive, subnormal or NaN
+    const uint32_t b = __float_as_uint(fabsf(s));
+    if (!(fabsf(s) >= 1.17549435e-38f)) return kMinExp;   // zero, subnormal or NaN
     const int e = (int)(b >> 23) - 127 + ((b & 0x7fffffu) ? 1 : 0);
     return min(e, 127);
 }

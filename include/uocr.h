@@ -426,7 +426,7 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  * the finite values of the rows this call adds,
  *   need = 2^max(ceil(log2(amax / 448)), -126);
  *   s = need, if the page holds no older row of the sequence, else
- *       max(s_old rounded up to a power of two, need);
+ *       max(|s_old| rounded up to a power of two, need), 2^127 at most;
  * a new value x is stored as e4m3(x / s), and where s != s_old the older rows'
  * codes c become e4m3(c * s_old / s), s_old finite.  Rounding, of codes and of the
  * rotated bf16 vectors alike, is to nearest even, once, from the value in 64 bits,

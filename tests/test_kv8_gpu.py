@@ -747,6 +747,28 @@ def test_append_codes_alike_in_both_kernels_over_many_values(uocr, cuda_device):
         assert torch.equal(a, b), int((a != b).sum())
 
 
+@pytest.mark.parametrize("old", [-0.25, -0.013, -3.0, -1e30, -1e-40, 0.0, 1e-40, 3e38, -3e38])
+@pytest.mark.parametrize("n", [1, 20])       # the kernel for few tokens; the one for many
+def test_append_to_a_page_of_any_finite_scale(uocr, cuda_device, old, n):
+    """Older rows keep their values (to e4m3's rounding under the new scale), also under a negative scale, which their
+    new codes' signs take up."""
+    H, lens = 3, [11 + n]
+    s, table, starts, _ = append_state(83, H, lens, [n])
+    page = int(table[0, 0])
+    s["k_scale"][page], s["v_scale"][page] = old, old
+    old = float(s["k_scale"][page, 0])
+    _, _, got = run_append(uocr, cuda_device, s, table, lens, starts)
+    rot = [ref.rotate(s["k_new"][i].double(), int(s["tok"][i]), int(s["page"][i])) for i in range(n)]
+    for x, rows in (("k", np.stack(rot)), ("v", s["v_new"].double().numpy())):
+        for h in range(H):
+            scale = max(ref.need_scale(rows[:, h]), min(ref.pow2_at_least(abs(old)), 2.0 ** 127))
+            assert float(got[x + "_scale"][page, h]) == scale
+            before = ref.GRID[s[x].view(torch.uint8).numpy()[page, h, :11]] * old
+            codes = got[x].view(torch.uint8)[page, h].numpy()
+            assert (ref.GRID[codes[:11]] == ref.GRID[ref.encode(before / scale)]).all()
+            assert (ref.GRID[codes[11:11 + n]] == ref.GRID[ref.encode(rows[:, h] / scale)]).all()
+
+
 def test_append_bad_sequences_are_skipped(uocr, cuda_device):
     lens = [40, 5, 96, 70]
     s, table, starts, n = append_state(7, 2, lens, [10, 5, 40, 3])
