@@ -85,6 +85,13 @@ __device__ __forceinline__ uint8_t to_e4m3(float x) {
     return (uint8_t)(r & 0xff);
 }
 
+// code * ratio rounded to odd: a ratio that is not a power of two has 24 bits, and a product of 28
+// rounded to fp32 first could reach a midpoint of e4m3 that it only lies beside.
+__device__ __forceinline__ float rescaled(float code, float ratio) {
+    const float p = __fmul_rz(code, ratio);
+    return fmaf(code, ratio, -p) != 0.f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+
 __device__ __forceinline__ float from_e4m3(uint8_t c) {
     const uint32_t h = e4m3x2_to_f16x2((uint16_t)c);
     return __low2float(*reinterpret_cast<const __half2 *>(&h));
@@ -215,7 +222,7 @@ rope_append_kv8_few_kernel(const __nv_bfloat16 *q, const __nv_bfloat16 *idx_q, c
             e = max(e, scale_exp_of(old));
             const float ratio = old / exp2i(e);
             if (ratio != 1.f)
-                for (int x = tid; x < run.row * kD; x += kAppThreads) codes[x] = to_e4m3(from_e4m3(codes[x]) * ratio);
+                for (int x = tid; x < run.row * kD; x += kAppThreads) codes[x] = to_e4m3(rescaled(from_e4m3(codes[x]), ratio));
         }
         const float inv = exp2i(1 - e);
         for (int x = tid; x < run.count * kD; x += kAppThreads)
@@ -270,8 +277,8 @@ __device__ __forceinline__ uint4 rescale_e4m3(uint4 v, float ratio) {
         const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
         const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
         uint16_t r0, r1;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r0) : "f"(a.y * ratio), "f"(a.x * ratio));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r1) : "f"(b.y * ratio), "f"(b.x * ratio));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r0) : "f"(rescaled(a.y, ratio)), "f"(rescaled(a.x, ratio)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r1) : "f"(rescaled(b.y, ratio)), "f"(rescaled(b.x, ratio)));
         out[w] = (uint32_t)r0 | (uint32_t)r1 << 16;
     }
     return make_uint4(out[0], out[1], out[2], out[3]);

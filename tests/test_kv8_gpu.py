@@ -769,6 +769,32 @@ def test_append_to_a_page_of_any_finite_scale(uocr, cuda_device, old, n):
             assert (ref.GRID[codes[11:11 + n]] == ref.GRID[ref.encode(rows[:, h] / scale)]).all()
 
 
+@pytest.mark.parametrize("n", [1, 20])       # the kernel for few tokens; the one for many
+def test_append_rescales_older_codes_with_one_rounding(uocr, cuda_device, n):
+    """Scales that take a code within 2^-24 of a midpoint of e4m3, on either side: 28 bits that round to the midpoint
+    itself in fp32."""
+    scales = [np.float32((k + 0.5) / c * 2.0 ** -j) for c in range(9, 16) for k in range(8, 16) for j in (3, 4)]
+    H, lens = len(scales) // 7, [11 + n]
+    for part in range(7):
+        s, table, starts, _ = append_state(84 + part, H, lens, [n])
+        page = int(table[0, 0])
+        for x in "kv":
+            s[x + "_scale"][page] = torch.tensor(scales[part * H:(part + 1) * H])
+            s[x][page, :, :11] = torch.arange(8, 16).repeat(16).float().to(ref.E4M3)      # 8 .. 15, exactly
+            s[x + "_new"] *= 2.0 ** -20                                                   # they do not raise the scale
+        _, _, got = run_append(uocr, cuda_device, s, table, lens, starts)
+        beside = 0
+        for x in "kv":
+            for h in range(H):
+                old, scale = float(s[x + "_scale"][page, h]), float(got[x + "_scale"][page, h])
+                assert scale == ref.pow2_at_least(old)
+                before = ref.GRID[s[x].view(torch.uint8).numpy()[page, h, :11]] * old / scale
+                codes = got[x].view(torch.uint8)[page, h, :11].numpy()
+                assert (ref.GRID[codes] == ref.GRID[ref.encode(before)]).all()
+                beside += int((ref.encode(before) != ref.encode(before.astype(np.float32))).sum())
+        assert beside > 0
+
+
 def test_append_bad_sequences_are_skipped(uocr, cuda_device):
     lens = [40, 5, 96, 70]
     s, table, starts, n = append_state(7, 2, lens, [10, 5, 40, 3])
