@@ -638,6 +638,17 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+def _int(x, name: str, most: int | None = None) -> int:
+    """x as the library's 32-bit integer; past `most`, where that means the same, `most`.  (ctypes would cut the upper
+    bits off without a word.)"""
+    x = int(x)
+    if most is not None and x > most:
+        return most
+    if not -(1 << 31) <= x < 1 << 31:
+        raise ValueError(f"{name} must fit in 32 bits, got {x}")
+    return x
+
+
 def _launch(fn, name: str, dev: int, stream, *args):
     """fn(*args, stream) with device `dev` current, on its current stream unless one is given."""
     if stream is None:
@@ -873,7 +884,7 @@ def dense_decode_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_len
     workspace = _space(workspace, lambda: dense_kv8_workspace_bytes(B, H, mb), dev, stream)
     _launch(_lib().uocr_dense_decode_kv8, "dense_decode_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            mb if ref_blocks is None else int(ref_blocks), B, H, mb, P, out.data_ptr(), _at(mass),
+            mb if ref_blocks is None else _int(ref_blocks, "ref_blocks", mb), B, H, mb, P, out.data_ptr(), _at(mass),
             workspace.data_ptr(), workspace.numel(), _at(dev_err))
     _lend(stream, out, workspace)
     return out
@@ -890,7 +901,7 @@ def sparse_attn_seq_kv8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     workspace = _space(workspace, lambda: sparse_attn_seq_kv8_workspace_bytes(n_q, H, mb), dev, stream)
     _launch(_lib().uocr_sparse_attn_seq_kv8, "sparse_attn_seq_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
-            int(seq), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
+            _int(seq, "seq"), q_pos.data_ptr(), sel.data_ptr(), n_q, B, H, mb, P, _SCALE if scale is None else float(scale),
             out.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
     _lend(stream, out, workspace)
     return out
@@ -906,8 +917,8 @@ def sparse_prefill_kv8(q, k_cache, v_cache, k_scale, v_scale, idx_q, idx_k_cache
     workspace = _space(workspace, lambda: prefill_kv8_workspace_bytes(n_q, H, mb), dev, stream)
     _launch(_lib().uocr_sparse_prefill_kv8, "sparse_prefill_kv8", dev, stream, q.data_ptr(), k_cache.data_ptr(),
             v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), idx_q.data_ptr(), idx_k_cache.data_ptr(),
-            block_table.data_ptr(), seq_lens.data_ptr(), int(seq), q_pos.data_ptr(), n_q, B, H, mb, P, out.data_ptr(),
-            sel.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
+            block_table.data_ptr(), seq_lens.data_ptr(), _int(seq, "seq"), q_pos.data_ptr(), n_q, B, H, mb, P,
+            out.data_ptr(), sel.data_ptr(), _at(mass), workspace.data_ptr(), workspace.numel(), _at(dev_err))
     _lend(stream, out, sel, workspace)
     return out, sel
 
@@ -955,8 +966,8 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
         _check_dev_err(dev_err, dev)
     workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev, stream)
     _launch(_lib().uocr_evict_blocks, "evict_blocks", dev, stream, mass.data_ptr(), block_table.data_ptr(),
-            seq_lens.data_ptr(), B, H, mb, int(keep_blocks), int(n_sink), new_mass.data_ptr(), new_table.data_ptr(),
-            new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            _at(dev_err))
+            seq_lens.data_ptr(), B, H, mb, _int(keep_blocks, "keep_blocks", (1 << 31) - 1), _int(n_sink, "n_sink"),
+            new_mass.data_ptr(), new_table.data_ptr(), new_lens.data_ptr(), freed.data_ptr(), n_freed.data_ptr(),
+            workspace.data_ptr(), workspace.numel(), _at(dev_err))
     _lend(stream, new_mass, new_table, new_lens, freed, n_freed, workspace)
     return new_mass, new_table, new_lens, freed, n_freed

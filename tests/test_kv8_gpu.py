@@ -1005,6 +1005,30 @@ def test_binding_refusals(uocr, cuda_device):
     assert uocr.sparse_attn_seq_kv8(q[:0], k, v, ks, vs, bt, sl, 0, seq[:0], sel[:0]).shape == (0, 2, 128)
 
 
+def test_integers_past_32_bits(uocr, cuda_device):
+    """Numbers of blocks past 32 bits mean what they say; a sequence or a sink past them is refused."""
+    c = Case([900, 700], 2, seed=23)
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    full = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl)
+    for big in (1 << 31, 1 << 32, (1 << 32) + 1, (1 << 63) - 1):
+        assert torch.equal(full, uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=big))
+        mass = c.mass.to(cuda_device)
+        got = uocr.evict_blocks(mass, bt, sl, big, n_sink=1)
+        assert torch.equal(got[0], mass) and torch.equal(got[1], bt) and torch.equal(got[2], sl) and (got[3] == -1).all() and (got[4] == 0).all()
+    pos, sel = (sl[:1] - 1).expand(2).contiguous(), c.select([899, 899]).to(cuda_device)
+    idx, idx_k = torch.zeros((2, 128), dtype=torch.bfloat16, device=cuda_device), torch.zeros((k.shape[0], 32, 128), dtype=torch.bfloat16, device=cuda_device)
+    for bad in (1 << 31, 1 << 32, (1 << 32) + 1, -(1 << 32)):
+        with pytest.raises(ValueError):
+            uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, bad, pos, sel)
+        with pytest.raises(ValueError):
+            uocr.sparse_prefill_kv8(q, k, v, ks, vs, idx, idx_k, bt, sl, bad, pos)
+        with pytest.raises(ValueError):
+            uocr.evict_blocks(c.mass.to(cuda_device), bt, sl, 8, n_sink=bad)
+    for call in (lambda: uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl, ref_blocks=-(1 << 32)), lambda: uocr.evict_blocks(c.mass.to(cuda_device), bt, sl, -(1 << 32) + 9)):
+        with pytest.raises(ValueError):
+            call()
+
+
 def test_matches_the_bf16_cache_of_the_same_values(uocr, cuda_device):
     """Power-of-two scales make every cached value a bf16 number, so both caches hold the same keys and values."""
     c = Case([700, 1500, 90], 10, seed=21)
