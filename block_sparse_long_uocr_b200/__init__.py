@@ -628,6 +628,11 @@ def _refuse(dev: int, *specs):
             raise ValueError(f"{name} must be on cuda:{dev} like the other tensors, got {t.device}")
 
 
+def _unfit():
+    """After `_refuse` found nothing to name: what an entry point asks for and the list of it do not agree."""
+    return ValueError("the tensors do not fit together (type, shape, device or density)")
+
+
 def _need(t, name: str):
     if t is None:
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -778,6 +783,7 @@ def rope_append_kv8(q, idx_q, k_new, v_new, idx_k_new, tok_pos, page_pos, block_
                 (_need(idx_k_cache, "idx_k_cache"), "idx_k_cache", _BF16, (P, BLOCK, IDX_DIM)),
                 (new_start, "new_start", _I32, (B + 1,)), (q_out, "q_out", _BF16, rows),
                 (idx_q_out, "idx_q_out", _BF16, idx))
+        raise _unfit()
     if dev_err is not None:
         _check_dev_err(dev_err, dev)
     _launch(_lib().uocr_rope_append_kv8, "rope_append_kv8", dev, stream, q.data_ptr(), idx_q.data_ptr(),
@@ -826,6 +832,7 @@ def _attn_args(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, per
                 (_need(seq_lens, "seq_lens"), "seq_lens", _I32, (B,)),
                 *_kv8_specs(k_cache, _need(v_cache, "v_cache"), _need(k_scale, "k_scale"), _need(v_scale, "v_scale"), P, H),
                 (out, "out", _BF16, (n, H, HEAD_DIM)), (mass, "mass", _F32, (B, H, mb)))
+        raise _unfit()
     if dev_err is not None:
         _check_dev_err(dev_err, dev)
     return dev, n, H, P, B, mb, out
@@ -962,6 +969,7 @@ def evict_blocks(mass, block_table, seq_lens, keep_blocks: int, *, n_sink: int =
                 (_need(seq_lens, "seq_lens"), "seq_lens", _I32, (B,)), (new_mass, "new_mass", _F32, (B, H, mb)),
                 (new_table, "new_table", _I32, (B, mb)), (new_lens, "new_lens", _I32, (B,)),
                 (freed, "freed", _I32, (B, mb)), (n_freed, "n_freed", _I32, (B,)))
+        raise _unfit()
     if dev_err is not None:
         _check_dev_err(dev_err, dev)
     workspace = _space(workspace, lambda: evict_workspace_bytes(B, H, mb), dev, stream)

@@ -128,6 +128,28 @@ def test_binding_refuses_before_any_launch(pkg):
         pkg.sparse_attn_kv8(None, k, k, s, s, bt, sl, torch.zeros((2, 16), dtype=torch.int32))
 
 
+def test_what_the_checks_refuse_is_never_launched(pkg, monkeypatch):
+    """Where the quick expression says no and the search for the culprit finds nothing, the call still ends there."""
+    launched = []
+    monkeypatch.setattr(pkg, "_refuse", lambda *a: None)
+    monkeypatch.setattr(pkg, "_dev", lambda t, *a: t)
+    monkeypatch.setattr(pkg, "_space", lambda *a: torch.empty(1, dtype=torch.uint8))
+    monkeypatch.setattr(pkg, "_launch", lambda *a: launched.append(a[1]))
+    q, x = torch.zeros((2, 3, 128), dtype=torch.bfloat16), torch.zeros((2, 128), dtype=torch.bfloat16)
+    k, s = torch.zeros((4, 3, 32, 128), dtype=torch.uint8).view(torch.float8_e4m3fn), torch.ones((4, 3))
+    bt, sl, ik = torch.zeros((2, 4), dtype=torch.int32), torch.ones(2, dtype=torch.int32), torch.zeros((4, 32, 128), dtype=torch.bfloat16)
+    sel, mass = torch.zeros((2, 16), dtype=torch.int32), torch.zeros((2, 3, 4))
+    out = dict(new_mass=mass.clone(), new_table=bt.clone(), new_lens=sl.clone(), freed=bt.clone(), n_freed=sl.clone())
+    for call in (lambda: pkg.rope_append_kv8(q, x, q, q, x, sl, sl, bt, sl, k, k, s, s, ik),
+                 lambda: pkg.sparse_attn_kv8(q, k, k, s, s, bt, sl, sel, out=q.clone()),
+                 lambda: pkg.dense_decode_kv8(q, k, k, s, s, bt, sl, out=q.clone()),
+                 lambda: pkg.sparse_attn_seq_kv8(q, k, k, s, s, bt, sl, 0, sl, sel, out=q.clone()),
+                 lambda: pkg.evict_blocks(mass, bt, sl, 4, **out)):
+        with pytest.raises(ValueError, match="do not fit together"):
+            call()
+    assert not launched
+
+
 # --------------------------------------------------------------------------- the plain forms themselves
 def test_encode_matches_torch_and_the_grid():
     x = torch.cat((torch.randn(4000) * 3, torch.randn(4000) * 1e-3, torch.linspace(-448, 448, 5001)))
