@@ -5,8 +5,8 @@
 // fp16 number exactly (4 significant bits, 2^-9 .. 448), so the tile products run on the fp16
 // tensor cores with fp32 accumulation and the scale is applied to their fp32 results: neither K
 // nor V is rounded again.  A query row is scaled by a power of two to fp16's range (exact, below);
-// a softmax weight is the sum of two fp16 numbers in two columns of B, which a single query leaves
-// free, so 22 bits of it are kept.
+// a softmax weight, at most 1 and relative to its block's largest, is the sum of two fp16 numbers in
+// two columns of B, which a single query leaves free: 22 bits of it are kept, down to 2^-25.
 //
 // The codes cannot go to the tensor cores as they are: mma.sync m16n8k32 on e4m3 operands runs on a
 // B200 as two fp16 MMAs and some 17 further instructions (counted: 23.6 issued per MMA with its

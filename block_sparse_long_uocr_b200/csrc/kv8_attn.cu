@@ -16,9 +16,11 @@ namespace uocr {
 
 namespace {
 
+constexpr float kLeast = -3.4028235e38f;   // the maximum over nothing: finite, so that it can be subtracted
+
 // A warp's softmax state over one or more blocks: acc of lane (g, 0) holds dims 16 g .. 16 g + 15.
 struct State8 {
-    float m = -INFINITY, l = 0.f;
+    float m = kLeast, l = 0.f;
     float acc[16];
     __device__ __forceinline__ State8() {
 #pragma unroll
@@ -43,10 +45,13 @@ __device__ __forceinline__ void load_scales8(Blocks8 &bl, const float *__restric
 }
 
 // Attention over the warp's blocks with a running maximum; done(t, m, l): the t-th block's weight
-// sum l in units of 2^m.  A block's K and V are loaded together and used at once; what overlaps the
-// arithmetic are the other warps' loads (16 to 20 a SM).  Loading the next block's K into the
-// registers that the scores free was slower (266 against 215 us for 16 x 32768 tokens): it keeps 32
-// more registers alive through the weighted sum, which then spills.
+// sum l in units of 2^m.  A block's weights are taken against its own maximum and meet the others' as
+// fp32 factors: against the running one, fp16 would keep few bits of the weights of a block far below
+// it, which count where its value scale is far above the others'.
+// A block's K and V are loaded together and used at once; what overlaps the arithmetic are the other
+// warps' loads (16 to 20 a SM).  Loading the next block's K into the registers that the scores free was
+// slower (266 against 215 us for 16 x 32768 tokens): it keeps 32 more registers alive through the
+// weighted sum, which then spills.
 template <class Done>
 __device__ __forceinline__ void attend8(State8 &st, const Blocks8 &bl, const uint4 *__restrict__ kc,
                                         const uint4 *__restrict__ vc, int H, int h, int p, float scale_log2,
@@ -73,23 +78,23 @@ __device__ __forceinline__ void attend8(State8 &st, const Blocks8 &bl, const uin
         float mb = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
-        const float m = fmaxf(st.m, mb);
-        const float base = m == -INFINITY ? 0.f : m;      // every score -inf: weights 0, not NaN
-        const float corr = exp2_approx(st.m - base);            // 0 on the first block
+        mb = fmaxf(mb, kLeast);   // every score -inf: weights 0, not NaN
+        const float ahead = st.m - mb, less = exp2_approx(-fabsf(ahead));
+        const float corr = ahead > 0.f ? 1.f : less, fresh = ahead > 0.f ? less : 1.f;   // of what was, of the block
         float w[4], lb = 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            w[i] = exp2_approx(z[i] - base);
+            w[i] = exp2_approx(z[i] - mb);
             lb += w[i];
         }
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) lb += __shfl_xor_sync(0xffffffffu, lb, x);
-        st.m = m;
-        st.l = fmaf(st.l, corr, lb);
+        st.m = fmaxf(st.m, mb);
+        st.l = fmaf(st.l, corr, lb * fresh);
 #pragma unroll
         for (int e = 0; e < 16; ++e) st.acc[e] *= corr;
-        weighted_sum8(st.acc, w, v, __shfl_sync(0xffffffffu, bl.vs, t), lane);
-        done(t, m, lb);
+        weighted_sum8(st.acc, w, v, __shfl_sync(0xffffffffu, bl.vs, t) * fresh, lane);
+        done(t, mb, lb);
     }
 }
 

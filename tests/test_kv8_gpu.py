@@ -470,6 +470,64 @@ def test_a_scale_that_is_not_finite_stays_with_its_rows(uocr, cuda_device, bad, 
                 assert ((again[2][:, 3].cpu() - rest[:, 3]).abs() <= 1e-4 * rest[:, 3].abs() + 1e-30).all(), name
 
 
+@pytest.mark.parametrize("form", ["sparse", "seq", "dense"])
+def test_light_blocks_under_large_value_scales(uocr, cuda_device, form):
+    """A block whose weights are 2^-23 of another's and whose value scale is 2^23 of the other's counts as much: its
+    weights keep their bits, whichever of the two a warp meets first."""
+    H, n, total = 10, 100, 32 * 32
+    c = Case([total] * (n if form != "seq" else 1), H, seed=96, n_q=n)
+    c.ks[:] = 2.0 ** -30
+    heavy = torch.zeros(c.k.shape[0], dtype=torch.bool)
+    heavy[c.table[:, [3, 17, 24]].long().flatten()] = True
+    c.q[:] = c.q.abs() + 1
+    c.k.view(torch.uint8)[heavy] = torch.tensor([1.0]).to(ref.E4M3).view(torch.uint8)      # q . k = sum of q, alike for a block's tokens
+    per = c.q.double().sum(-1) * 128 ** -0.5
+    c.ks[heavy] = float(23 * math.log(2) / per.mean())
+    c.vs[heavy] *= 2.0 ** -23
+    c.v.view(torch.uint8)[:] &= 0x7F      # of one sign, so that a weight's error shows
+    q, k, v, ks, vs, bt, sl = c.gpu(cuda_device)
+    blocks = [0, 3, 5, 8, 9, 11, 12, 13, 16, 17, 20, 21, 23, 24, 27, 31]
+    se = torch.tensor([blocks] * n, dtype=torch.int32, device=cuda_device)
+    if form == "sparse":         # 1000 pairs: a warp attends four blocks
+        out = uocr.sparse_attn_kv8(q, k, v, ks, vs, bt, sl, se)
+    elif form == "seq":
+        out = uocr.sparse_attn_seq_kv8(q, k, v, ks, vs, bt, sl, 0, torch.full((n,), total - 1, dtype=torch.int32, device=cuda_device), se)
+    else:
+        out, blocks = uocr.dense_decode_kv8(q, k, v, ks, vs, bt, sl), list(range(32))
+    out = out.float().cpu().double()
+    for i in range(0, n, 7):
+        o, w, mag, vmax, _ = c.want(i, i if form != "seq" else 0, total - 1, blocks, 128 ** -0.5)
+        # what the light blocks' values add, with the weights' error (2^-22 of a weight in two fp16 numbers; 2^-11 in one
+        # and as much of a partial output; ref.weight_bound for the fp32 part), bf16's half step
+        light = torch.tensor([not bool(heavy[int(c.table[i if form != "seq" else 0, j])]) for j in blocks])
+        size = w[:, light].sum(-1) * vmax + 2.0 ** -23 * vmax
+        lim = o.abs() * 2.0 ** -8 + (size * (ref.weight_bound(mag) + (2.0 ** -10 if form == "seq" else 2.0 ** -22)))[:, None]
+        assert ((out[i] - o).abs() <= lim).all(), (i, float(((out[i] - o).abs() / lim).max()))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+def test_a_query_that_is_not_finite_stays_its_own_in_every_form(uocr, cuda_device, bad):
+    """Its row and head is NaN, its weights add nothing; every other row, head and total is what it is without it."""
+    c = Case([450], 10, seed=97, n_q=100)
+    fine = c.q.clone()
+    for name, out, mass, rows, many in every_form(uocr, cuda_device, c, 100, None):
+        hit = torch.zeros((len(rows), 10), dtype=torch.bool)
+        for i, h in ((0, 3), (2, 9), (17, 0)):
+            if i < len(rows):
+                c.q[i, h, 11 * h + 5], hit[i, h] = bad, True
+        again = dict((x[0], x) for x in every_form(uocr, cuda_device, c, 100, None))[name]
+        c.q = fine.clone()
+        got = again[1].float().cpu()
+        assert torch.isnan(got[hit]).all() and torch.equal(got[~hit], out.float().cpu()[~hit]), name
+        if mass is not None:
+            total = c.mass.double()
+            for i, b, p, x in rows:
+                _, w, _, _, used = c.want(i, b, p, x, 128 ** -0.5)
+                for y, j in enumerate(used):
+                    total[b, :, j] += torch.where(hit[i], 0.0, w[:, y])
+            assert ((again[2].cpu().double() - total).abs() <= 1e-4 * total + 1e-30).all(), name
+
+
 @pytest.mark.parametrize("n", [5, 100])      # a query at a time; block by block
 @pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1e-3, 30.0, 1e7, 1e8, 1e9, 1e20])
 def test_many_queries_of_any_magnitude(uocr, cuda_device, n, q_scale):
