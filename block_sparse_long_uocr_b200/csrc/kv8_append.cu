@@ -133,6 +133,7 @@ __device__ __forceinline__ bool find_run(int r, const int32_t *__restrict__ star
     }
     if (a == e) return false;
     const int len = __ldg(seq_lens + b);
+    if (!start && len == 0) return false;   // an empty place of a padded batch has no new token
     if (len < e - a || len > max_blocks * kBlock) {
         if (report) flag_error(dev_err, UOCR_DEVERR_POS);
         return false;

@@ -397,6 +397,8 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  * finite scale, negative ones and 0 too; the writer below makes powers of two.  A
  * (page, head) with a k_scale that is not finite makes the rows that attend it NaN,
  * one with such a v_scale makes them NaN or infinite; other rows are not touched.
+ * Weighted values are summed in fp32 before the sum is divided by the weights':
+ * values above 2^110 in magnitude may leave its range.
  *
  * mass, fp32 [B][H][max_blocks], optional (NULL: not kept): running totals of
  * the attention weight that each block received, the input of
@@ -415,9 +417,10 @@ uocr_status_t uocr_sparse_decode_static(const void *q, const void *k_cache, cons
  * uocr_rope_append over the 8-bit cache: page2d rotation of n new tokens and
  * their append.  Sequence b's new tokens are rows new_start[b] ..
  * new_start[b+1] - 1 of q, k_new, ... (new_start int32 [B+1], ascending from
- * 0 to at most n; NULL: n == B and token i belongs to sequence i), at the
- * sequence's last positions: seq_lens already counts them.  Rows past
- * new_start[B] are not touched.
+ * 0 to at most n; NULL: n == B and token i belongs to sequence i, whose place in
+ * the batch is empty if its length is 0), at the sequence's last positions:
+ * seq_lens already counts them.  Rows past new_start[B] and those of empty places
+ * are not touched.
  *   q [n][H][128], idx_q [n][128]   rotated into q_out, idx_q_out (which may be
  *                                   q, idx_q themselves; no other overlap)
  *   k_new, v_new [n][H][128]        rotated k and raw v, quantised

@@ -853,6 +853,22 @@ def test_append_rescales_older_codes_with_one_rounding(uocr, cuda_device, n):
         assert beside > 0
 
 
+def test_append_to_a_padded_batch(uocr, cuda_device):
+    """One token a sequence, some places of the batch empty: nothing of theirs is touched and nothing flagged; a length
+    below 0 still is."""
+    lens, H = [33, 0, 1, 0, 64], 3
+    s, table, starts, n = append_state(92, H, lens, [1] * 5)
+    err = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    got = run_append(uocr, cuda_device, s, table, lens, None, dev_err=err, null_start=True)
+    assert int(err) == 0
+    want = ref.append(s, starts, lens, table)
+    check_append(s, got, want, (torch.full_like(s["q"], 7.0), torch.full_like(s["idx_q"], 7.0)))
+    assert (got[0][[1, 3]] == 7).all() and (got[1][[1, 3]] == 7).all()
+    lens[3] = -1
+    run_append(uocr, cuda_device, s, table, lens, None, dev_err=err, null_start=True)
+    assert int(err) == uocr.DEVERR_POS
+
+
 def test_append_bad_sequences_are_skipped(uocr, cuda_device):
     lens = [40, 5, 96, 70]
     s, table, starts, n = append_state(7, 2, lens, [10, 5, 40, 3])
