@@ -557,8 +557,12 @@ evict_compact_kernel(const float *mass, const int32_t *__restrict__ dst, const i
 namespace {
 // CTAs per sequence of the one-launch form (a CTA takes an SM's threads): at most 4, as long as all
 // sequences' fit on the SMs at once, and more where only a smaller slice fits in shared memory; 0
-// where none does.  Measured at 64 sequences of 4096 blocks and at 3 of 777, 10 to 12 heads (us):
-// 1 CTA 23.8 / 8.5, 2: 18.0 / 7.8, 4: 26.5 / 7.6; the three-launch form 30.5 / 13.8.
+// where none does.  Measured with 1 / 2 / 4 / 8 CTAs and with three launches (us; sequences x blocks, 10
+// heads unless given): 1 x 4096 - / 12.4 / 10.9 / 10.2, 20.7; 8 x 4096 - / 12.7 / 11.1 / 10.5, 21.6; 64 x 4096
+// - / 13.2 / 21.8 / 40.4, 26.9; 32 x 2048 10.9 / 9.5 / 9.0 / 18.6, 17.5; 16 x 2048 (16 heads) 13.3 / 11.1 / 9.9 /
+// 13.8, 16.7; 64 x 1024 8.7 / 7.9 / 14.7 / 30.9, 17.5; 128 x 512 7.7 / 13.9 / 26.5 / 52.9, 18.9; 3 x 777 (12
+// heads) 8.2 / 7.8 / 7.8 / 7.8, 11.1.  Three launches where nothing fits: 8 x 20480 68, 16 x 32768 131 (floors
+// 2.3 and 7.4: one CTA a sequence selects, one a row moves).
 constexpr size_t kRoom = 192 * 1024;   // shared memory of the slice and the keys
 int evict_ctas(int B, int H, int max_blocks, int num_sms) {
     int ctas = 4;

@@ -29,9 +29,10 @@
 //   many: CTA (run, a few heads), thread (token, 8 pairs) of 32 tokens: the sines of a page are
 //       formed once for the CTA's heads and kept in registers, every load and store is 8 or 16 bytes.
 //       2048 tokens, 10 heads: 27.7 us with the first kernel (11 times the sines, 64-bit conversions
-//       at 16 a clock), 15.4 here: bound by the issue of the rotation's two-number products (about
-//       1000 instructions a thread and head) and one barrier a head, not by its 28 MB (4.3 us).  1.4 of
-//       them are what the queries' single rounding costs (a test of each value in fp32).
+//       at 16 a clock), 15.4 here: bound by the issue of the rotation's two-number products (1260
+//       instructions a warp and head, its share of the sines counted; 45 % of the issue slots) and one
+//       barrier a head, not by its 28 MB (4.3 us).  1.5 of the 15.4 are what the queries' single rounding
+//       costs (a test of each value in fp32).
 #include <math.h>
 
 #include "kernels.h"
@@ -487,9 +488,10 @@ cudaError_t launch_rope_append_kv8(const LaunchCtx &c, const void *q, const void
                                    float *v_scale, void *idx_k_cache, int32_t *dev_err) {
     const long long runs = start ? (long long)n / kBlock + 2ll * B : n;
     if (runs > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    // Measured with few / many (us, 10 heads; sequences x tokens): 1 x 4 4.8 / 5.0, 1 x 8 6.5 / 5.1,
-    // 1 x 2048 27.7 / 14.5, 16 x 4 6.1 / 6.2, 16 x 8 8.2 / 6.8, 64 x 1 4.6 / 9.8, 64 x 8 12.5 / 13.0,
-    // 64 x 16 19.8 / 13.7.
+    // Measured with few / many (us, 10 heads; sequences x tokens): 1 x 4 4.7 / 5.9, 1 x 8 6.3 / 6.0, 1 x 64
+    // 16.2 / 6.4, 1 x 2048 26.8 / 15.4, 16 x 4 6.1 / 6.8, 16 x 6 7.2 / 7.1, 16 x 8 8.0 / 7.1, 64 x 1 4.4 / 10.1,
+    // 64 x 6 10.9 / 14.4, 64 x 8 11.8 / 14.3, 64 x 16 19.1 / 15.2: the border lies at 6 to 7 tokens a sequence
+    // for few sequences, at some 11 for 64.
     if ((long long)n > 6ll * B) {
         // about two CTAs a SM: more would form the same sines more often
         const int groups = (int)min((long long)H + 1, max(1ll, 2ll * c.num_sms / (n / kBlock + B)));

@@ -18,8 +18,8 @@
 //                not depend on the order of the atomics);
 //   5. totals    the sums of step 4 added to the running totals.
 // A few queries are attended one by one instead (sparse_attn_kv8_kernel); their weights go the same way.
-// Roundings to fewer than 32 bits: the weights p in [0, 1] to fp16 for P V (2^-11 relative, their
-// sum l keeps 32 bits) and the partial outputs to fp16 (2^-11; |acc| <= 32 * 448, in units of the
+// Roundings to fewer than 32 bits: the weights p in [0, 1] to fp16 for P V (2^-11 relative, 2^-25 of the
+// block's largest at the least; their sum l keeps 32 bits) and the partial outputs to fp16 (2^-11; |acc| <= 32 * 448, in units of the
 // block's value scale, so fp16 holds it): each an eighth of the output's own rounding to bf16.
 //
 // Staging of step 3, per warp: a K tile and a V tile by TMA in the 128-byte swizzle (16-byte piece p

@@ -489,8 +489,8 @@ uocr_status_t uocr_dense_decode_kv8(const void *q, const void *k_cache, const vo
  * uocr_sparse_attn_seq over the 8-bit cache: n_q queries of sequence `seq`,
  * each over its own selection, every selected (block, head) tile read once for
  * all of them.  The softmax weights go to the tensor cores in fp16 and each
- * slot's partial output is kept in fp16 (2^-11 relative each); weight sums stay
- * fp32.  A few queries (n_q * H up to 5 per SM) are attended one by one, as in
+ * slot's partial output is kept in fp16 (2^-11 relative each, or 2^-25 of the block's
+ * largest weight); weight sums stay fp32.  A few queries (n_q * H up to 5 per SM) are attended one by one, as in
  * uocr_sparse_attn_kv8.  With mass, row `seq` receives the sum over the n_q
  * queries, each weight as a multiple of 2^-40; n_q above 2^23 is then
  * UOCR_ERR_UNSUPPORTED, and so is num_pages * H above 2^31 - 1 with or without.
