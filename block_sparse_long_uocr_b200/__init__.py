@@ -35,6 +35,7 @@ Entry points (same names as the C ABI, without the ``uocr_`` prefix):
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -238,7 +239,26 @@ def alloc_workspace(n_q: int, heads: int, max_blocks: int, device) -> torch.Tens
     return torch.empty(max(workspace_bytes(n_q, heads, max_blocks), 1), dtype=torch.uint8, device=device)
 
 
+def _on_its_stream(fn):
+    """What `fn` allocates and fills is allocated for, and filled on, the stream that it is given: memory or fills of the
+    current stream would not be ordered before the kernels.  What it returns may be used on the current stream and
+    dropped there."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        current = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            got = fn(*args, stream=stream, **kw)
+        for t in got if isinstance(got, tuple) else (got,):
+            t.record_stream(current)
+        return got
+
+    return call
+
+
 # --------------------------------------------------------------------------- entry points
+@_on_its_stream
 def index_score(idx_q, idx_k_cache, block_table, seq_lens, q_seq=None, q_pos=None, *,
                 scores=None, dev_err=None, stream=None) -> torch.Tensor:
     """fp32 [n_q, max_blocks] block scores (entries past a query's causal blocks untouched)."""
@@ -261,6 +281,7 @@ def index_score(idx_q, idx_k_cache, block_table, seq_lens, q_seq=None, q_pos=Non
     return scores
 
 
+@_on_its_stream
 def block_topk(scores, seq_lens, q_seq=None, q_pos=None, *, sel=None, dev_err=None, stream=None) -> torch.Tensor:
     """int32 [n_q, 16] selected logical blocks (ascending, -1 padded)."""
     _dev(scores, "scores", torch.float32, 2)
@@ -276,6 +297,7 @@ def block_topk(scores, seq_lens, q_seq=None, q_pos=None, *, sel=None, dev_err=No
     return sel
 
 
+@_on_its_stream
 def sparse_attn(q, k_cache, v_cache, block_table, seq_lens, sel, q_seq=None, q_pos=None, *,
                 scale: float | None = None, out=None, dev_err=None, stream=None) -> torch.Tensor:
     """bf16 [n_q, H, 128] attention output over the selected blocks."""
@@ -303,6 +325,7 @@ def sparse_attn(q, k_cache, v_cache, block_table, seq_lens, sel, q_seq=None, q_p
     return out
 
 
+@_on_its_stream
 def sparse_decode(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_lens, *,
                   out=None, sel=None, workspace=None, dev_err=None, stream=None):
     """One decode query per sequence at p = seq_len - 1.  Returns (out [B,H,128] bf16, sel [B,16] int32)."""
@@ -331,6 +354,7 @@ def sparse_decode(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_lens
     return out, sel
 
 
+@_on_its_stream
 def prefill_index_score(idx_q, idx_k_cache, block_table, seq_lens, seq: int, q_pos, *,
                         scores=None, dev_err=None, stream=None) -> torch.Tensor:
     """fp32 [n_q, max_blocks] block scores of n_q queries of sequence `seq` (tcgen05 GEMM)."""
@@ -354,6 +378,7 @@ def prefill_index_score(idx_q, idx_k_cache, block_table, seq_lens, seq: int, q_p
     return scores
 
 
+@_on_its_stream
 def sparse_prefill(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_lens, seq: int, q_pos, *,
                    out=None, sel=None, workspace=None, dev_err=None, stream=None):
     """Prefill chunk of sequence `seq`.  Returns (out [n_q,H,128] bf16, sel [n_q,16] int32)."""
@@ -387,6 +412,7 @@ def sparse_prefill(q, k_cache, v_cache, idx_q, idx_k_cache, block_table, seq_len
     return out, sel
 
 
+@_on_its_stream
 def sparse_attn_seq(q, k_cache, v_cache, block_table, seq_lens, seq: int, q_pos, sel, *, scale=None,
                     out=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
     """Attention of many queries of sequence `seq` over the given selection (block-centric).
@@ -418,6 +444,7 @@ def sparse_attn_seq(q, k_cache, v_cache, block_table, seq_lens, seq: int, q_pos,
     return out
 
 
+@_on_its_stream
 def summary_score(idx_q, summary_cache, block_table, seq_lens, q_seq=None, q_pos=None, *,
                   scores=None, dev_err=None, stream=None) -> torch.Tensor:
     """fp32 [n_q, max_blocks]: idx_q . summary of each causal block's page."""
@@ -440,6 +467,7 @@ def summary_score(idx_q, summary_cache, block_table, seq_lens, q_seq=None, q_pos
     return scores
 
 
+@_on_its_stream
 def block_summary_mean(idx_k_cache, summary_cache=None, pages=None, *, dev_err=None, stream=None) -> torch.Tensor:
     """bf16 [P, 128]: the mean of each (listed) page's indexer keys."""
     _dev(idx_k_cache, "idx_k_cache", torch.bfloat16, 3)
@@ -455,6 +483,7 @@ def block_summary_mean(idx_k_cache, summary_cache=None, pages=None, *, dev_err=N
     return summary_cache
 
 
+@_on_its_stream
 def sparse_decode_summary(q, k_cache, v_cache, idx_q, summary_cache, block_table, seq_lens, *,
                           out=None, sel=None, workspace=None, dev_err=None, stream=None):
     """sparse_decode with block-summary scoring.  Returns (out, sel)."""
@@ -482,6 +511,7 @@ def sparse_decode_summary(q, k_cache, v_cache, idx_q, summary_cache, block_table
     return out, sel
 
 
+@_on_its_stream
 def block_topk_masked(scores, seq_lens, cand_mask, q_seq=None, q_pos=None, *, sel=None, dev_err=None,
                       stream=None) -> torch.Tensor:
     """Selection where remote candidate j of sequence b needs bit j of cand_mask[b] (int32 words)."""
@@ -535,6 +565,7 @@ def dense_workspace_bytes(n_q: int, heads: int, max_blocks: int) -> int:
     return int(_lib().uocr_dense_workspace_bytes(int(n_q), int(heads), int(max_blocks)))
 
 
+@_on_its_stream
 def dense_decode(q, k_cache, v_cache, block_table, seq_lens, *, ref_blocks: int | None = None,
                  out=None, workspace=None, dev_err=None, stream=None) -> torch.Tensor:
     """Decode attention over blocks [0, ref_blocks) plus the 4-block local window (all blocks when

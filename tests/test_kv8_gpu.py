@@ -1300,7 +1300,7 @@ def test_a_call_on_another_stream_takes_no_memory_with_work_queued_on_the_curren
         temps = [torch.full((x,), 0x5A, dtype=torch.uint8, device=cuda_device) for x in sizes]
         keep = [torch.zeros_like(t) for t in temps]
         torch.cuda.synchronize()
-        torch.cuda._sleep(20_000_000)
+        torch.cuda._sleep(80_000_000)
         for a, b in zip(keep, temps):
             a.copy_(b)
         del temps, a, b
